@@ -75,12 +75,15 @@ extern "C" {
 #define PKV_DEVERR_BAD_PAGE 1 /* a block-table entry outside [0, num_pages) */
 #define PKV_DEVERR_BAD_LEN 2  /* a length < 0 or > max_blocks * page_size */
 #define PKV_DEVERR_TIMEOUT 4  /* a bounded pipeline wait gave up (nothing hung) */
+#define PKV_DEVERR_BAD_AXIS 8 /* attn_qk_norm_rope_append: a pair_axis entry outside [0, n_axes) */
 
 /* Support set of this build (others return PKV_ERR_UNSUPPORTED):
  *   decode / cascade : head_dim 64 or 128; page_size 16; group size 1, 2, 4 or 8;
  *                      PKV_F32 or PKV_BF16 (cascade: PKV_BF16, head_dim 128)
  *   prefill          : head_dim 128; PKV_BF16; any seq_len >= 1
  *   flat GEMM        : PKV_BF16; 1 <= m <= 64; k a multiple of 8
+ *   append           : head_dim 64 or 128; page_size 16; PKV_F32 or PKV_BF16; any head counts
+ *   accumulated weights, eviction : as decode (eviction: any head count)
  */
 
 /* Human-readable name of a status code. Static storage; never NULL. */
@@ -384,6 +387,117 @@ int attn_decode_cascade(const void* q, const void* k_pages, const void* v_pages,
  */
 int attn_flat_gemm(const void* x, const void* w, void* y, int m, int n, int k, int dtype,
                    int32_t* err_flag, void* stream);
+
+/*
+ * Write of new tokens into the paged cache, with the per-head norms and the rotary position
+ * rotation of queries and keys in the same pass: what runs between the QKV projection and
+ * attn_decode_paged (chunk_len 1) or attn_prefill_paged_chunk. New token i of sequence b
+ * goes to cache position prefix_lens[b] + i. For every query and key head row x:
+ *   y = x * rsqrt(mean(x^2) + norm_eps) * norm[head_dim]      (q_norm / k_norm; NULL: y = x)
+ *   a pair (a, b) of y turns by t = position[axis] * inv_freq[pair]:
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+ * in fp32, rounded once. Values are copied. Elements from rotary_dim on are not rotated.
+ *
+ *   q, k, v      : dtype; token t = b * chunk_len + i at q + t * q_stride (k_stride, v_stride;
+ *                  in elements), its [n_qo_heads] ([n_kv_heads]) rows of head_dim contiguous
+ *                  from there, so q, k and v may be slices of one fused projection. Strides
+ *                  are multiples of 4 elements, at least heads * head_dim; pointers aligned
+ *                  to 4 elements (16 bytes for PKV_F32, 8 for PKV_BF16)
+ *   q_norm, k_norm : dtype [head_dim], or NULL for no norm; aligned like q
+ *   inv_freq     : fp32 [rotary_dim / 2], radians per position (finite; another value makes
+ *                  its pair NaN); may be NULL when rotary_dim is 0
+ *   rotary_dim   : 0 (no rotation) or a multiple of 8, at most head_dim
+ *   interleaved  : 0: pair p is elements (p, p + rotary_dim / 2); 1: (2 p, 2 p + 1)
+ *   positions    : int32 [n_axes][batch][chunk_len] (any value, also negative), or NULL:
+ *                  prefix_lens[b] + i on every axis. They are separate from the cache
+ *                  positions, which fall behind once attn_cache_evict has shortened a cache
+ *   pair_axis    : int32 [rotary_dim / 2], the axis (0 .. n_axes - 1) that each pair turns
+ *                  by, e.g. time, height and width; NULL: axis 0. 1 <= n_axes <= 4. An entry
+ *                  outside the range sets PKV_DEVERR_BAD_AXIS and makes its pair NaN
+ *   chunk_lens   : int32 [batch], new tokens of each sequence (0 .. chunk_len), the rest of
+ *                  its row being padding; NULL: chunk_len each
+ *   q_out        : dtype [batch][chunk_len][n_qo_heads][head_dim], contiguous, aligned like
+ *                  q; may be q itself when q_stride = n_qo_heads * head_dim. Padding rows are
+ *                  left as they were
+ *   k_pages, v_pages, block_table : the paged layout above (16-byte aligned pools)
+ * A sequence with prefix_lens[b] < 0, chunk_lens[b] outside its range, or prefix_lens[b] +
+ * chunk_lens[b] past the table sets PKV_DEVERR_BAD_LEN, a bad table entry
+ * PKV_DEVERR_BAD_PAGE; the q_out rows of such tokens are NaN and their K and V are not
+ * written. Two new tokens must not share a cache slot. Angles are taken modulo a turn exactly
+ * (fixed point), so far positions lose no precision.
+ */
+int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const void* q_norm,
+                             const void* k_norm, float norm_eps, const float* inv_freq,
+                             int rotary_dim, int interleaved, const int32_t* positions, int n_axes,
+                             const int32_t* pair_axis, const int32_t* block_table,
+                             const int32_t* prefix_lens, const int32_t* chunk_lens, void* q_out,
+                             void* k_pages, void* v_pages, int batch, int chunk_len,
+                             int max_blocks_per_seq, int num_pages, int n_qo_heads, int n_kv_heads,
+                             int head_dim, int page_size, int dtype, int32_t* err_flag,
+                             void* stream);
+
+/*
+ * Accumulated attention weights: how much softmax weight every cached token has received,
+ * summed over decode steps (and prompt chunks) per KV head, which is what
+ * attn_cache_evict ranks tokens by.
+ *
+ *   sums : fp32 [batch][n_kv_heads][max_blocks_per_seq * page_size], row b in step with row b
+ *          of the block table; 16-byte aligned
+ *
+ * attn_decode_paged_weights is attn_decode_paged that also adds the step's weights:
+ *   sums_out[b][g][t] = decay * sums_in[b][g][t] + sum_{h in group g} exp(scale q_h . k_t - lse_h)
+ * for t < kv_lens[b]; slots at or past the length are neither read nor written, so the sums of
+ * the newest token must have been set (to 0) before. sums_out may be sums_in (in place), and
+ * must not overlap it otherwise. decay is finite (1: plain accumulation). out, lse, splits and
+ * errors are as for attn_decode_paged; a row that came out NaN makes its group's sums NaN, and
+ * a bad length leaves the sequence's sums as they were. workspace: at least
+ * attn_decode_weights_workspace_size bytes, 256-byte aligned: the split partials, the call's
+ * logits (fp32 [batch][n_qo_heads][max_blocks_per_seq * page_size]) and log-sum-exps.
+ */
+size_t attn_decode_weights_workspace_size(int batch, int max_blocks_per_seq, int n_qo_heads,
+                                          int n_kv_heads, int head_dim, int page_size,
+                                          int num_splits, int dtype);
+
+int attn_decode_paged_weights(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* kv_lens, void* out,
+                              float* lse, const float* sums_in, float* sums_out, int batch,
+                              int max_blocks_per_seq, int num_pages, int n_qo_heads,
+                              int n_kv_heads, int head_dim, int page_size, float scale, float decay,
+                              int num_splits, int dtype, void* workspace, size_t workspace_bytes,
+                              int32_t* err_flag, void* stream);
+
+/*
+ * Eviction from the paged cache: every sequence is cut to at most `budget` tokens per KV head.
+ * A KV head of a sequence with n = kv_lens[b] > budget tokens keeps the first n_sink, the last
+ * n_recent and, of those between, the budget - n_sink - n_recent with the largest sums (equal
+ * sums: the lower index first; NaN counts as the largest), in their order; with n <= budget it
+ * keeps all. The kept rows of K and V are copied into the pages of new_block_table, in the same
+ * pools, and the caller then goes on with the new table, lengths and sums and frees the old
+ * pages. Heads keep different tokens, so cache positions say nothing about token positions
+ * any more: attn_qk_norm_rope_append takes those separately.
+ *
+ *   block_table     : int32 [batch][max_blocks_per_seq], kv_lens: int32 [batch]
+ *   sums            : fp32 [batch][n_kv_heads][max_blocks_per_seq * page_size]
+ *   new_block_table : int32 [batch][new_max_blocks]; new_max_blocks * page_size >= budget. The
+ *                     first ceil(min(n, budget) / page_size) entries of a row are used; those
+ *                     pages must not occur in the old pages in use, nor twice (a page that does
+ *                     is left with mixed contents). Old pages may be shared between sequences
+ *   kept            : int32 [batch][n_kv_heads][budget], out: old index of new token j, -1 at
+ *                     and past the new length
+ *   new_lens        : int32 [batch], out: min(n, budget)
+ *   new_sums        : fp32 [batch][n_kv_heads][new_max_blocks * page_size], out: the kept
+ *                     tokens' sums, 0 at and past the new length
+ * Outputs must not overlap inputs. A length < 0 or past the table sets PKV_DEVERR_BAD_LEN and
+ * counts as 0. A bad entry of block_table sets PKV_DEVERR_BAD_PAGE and makes the rows NaN; a bad
+ * entry of new_block_table sets it too and its rows are not copied.
+ */
+int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
+                     const int32_t* kv_lens, const float* sums, const int32_t* new_block_table,
+                     int32_t* kept, int32_t* new_lens, float* new_sums, int batch,
+                     int max_blocks_per_seq, int new_max_blocks, int num_pages, int n_kv_heads,
+                     int head_dim, int page_size, int budget, int n_sink, int n_recent, int dtype,
+                     int32_t* err_flag, void* stream);
 
 /*
  * Failure-handling hook for tests (the pages have no counterpart). It lets a test make a

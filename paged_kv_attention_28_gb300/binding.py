@@ -28,6 +28,7 @@ PKV_ERR_DEVICE = -5
 PKV_DEVERR_BAD_PAGE = 1
 PKV_DEVERR_BAD_LEN = 2
 PKV_DEVERR_TIMEOUT = 4
+PKV_DEVERR_BAD_AXIS = 8
 
 EXPORTS = [
     "attn_status_string", "attn_last_cuda_error_string", "attn_decode_num_splits", "attn_decode_workspace_size",
@@ -35,6 +36,8 @@ EXPORTS = [
     "attn_prefill_causal", "attn_cascade_workspace_size", "attn_decode_cascade",
     "attn_decode_paged_noalloc", "attn_decode_paged_fp8", "attn_prefill_paged_chunk",
     "attn_flat_gemm", "attn_flat_gemm_num_splits", "attn_debug_decode_stall",
+    "attn_qk_norm_rope_append", "attn_decode_weights_workspace_size", "attn_decode_paged_weights",
+    "attn_cache_evict",
 ]
 
 
@@ -84,6 +87,16 @@ def _load() -> ctypes.CDLL:
                                         [f32, i32, vp, sz, vp, vp])
     lib.attn_flat_gemm.restype = i32
     lib.attn_flat_gemm.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    i64 = ctypes.c_int64
+    lib.attn_qk_norm_rope_append.restype = i32
+    lib.attn_qk_norm_rope_append.argtypes = ([vp] * 3 + [i64] * 3 + [vp, vp, f32, vp, i32, i32, vp, i32] + [vp] * 7 +
+                                             [i32] * 9 + [vp, vp])
+    lib.attn_decode_weights_workspace_size.restype = sz
+    lib.attn_decode_weights_workspace_size.argtypes = [i32] * 8
+    lib.attn_decode_paged_weights.restype = i32
+    lib.attn_decode_paged_weights.argtypes = [vp] * 9 + [i32] * 7 + [f32, f32, i32, i32, vp, sz, vp, vp]
+    lib.attn_cache_evict.restype = i32
+    lib.attn_cache_evict.argtypes = [vp] * 9 + [i32] * 11 + [vp, vp]
     lib.attn_debug_decode_stall.restype = i32
     lib.attn_debug_decode_stall.argtypes = [i32, ctypes.c_ulonglong]
     lib.attn_flat_gemm_num_splits.restype = i32
@@ -352,6 +365,155 @@ def flat_gemm(x, w, out=None, err_flag=None, stream=None):
     st = lib.attn_flat_gemm(_ptr(x), _ptr(w), _ptr(out), m, n, k, _dt(x), _ptr(err_flag), _stream(stream))
     _check(st, "attn_flat_gemm")
     return out
+
+
+# --------------------------------------------------------------------------- cache write
+
+def _here(t: torch.Tensor, name: str):
+    """The library launches on the current device: its tensors have to be there."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Checks ``[B, C, H, D]`` whose head rows are contiguous per token; the token stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    B, C, H, D = shape
+    sb, sc, sh, sd = t.stride()
+    token = sc if C > 1 else sb if B > 1 else H * D
+    if (sd != 1 and D > 1) or (sh != D and H > 1) or (B > 1 and C > 1 and sb != C * sc):
+        raise ValueError(f"{name} must hold each token's heads contiguously at one stride per token, got {t.stride()}")
+    return token
+
+
+def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chunk_lens=None, positions=None,
+                        inv_freq=None, pair_axis=None, q_norm=None, k_norm=None, eps=1e-6, interleaved=False,
+                        out=None, err_flag=None, stream=None):
+    """Norm, rotate and write new tokens into the pages through ``attn_qk_norm_rope_append``.
+
+    ``q`` ``[B, C, Hq, D]`` and ``k``, ``v`` ``[B, C, Hkv, D]`` may be slices of one fused
+    projection; ``positions`` ``[n_axes, B, C]`` (or ``[B, C]`` for one axis). Returns the
+    rotated queries ``[B, C, Hq, D]``."""
+    B, C, Hq, D = q.shape
+    num_pages, Hkv, P, D2 = k_pages.shape
+    assert D2 == D
+    max_blocks = block_table.shape[1]
+    qs = _token_rows(q, "q", q.dtype, (B, C, Hq, D))
+    ks = _token_rows(k, "k", q.dtype, (B, C, Hkv, D))
+    vs = _token_rows(v, "v", q.dtype, (B, C, Hkv, D))
+    _here(q, "q")
+    _need(k_pages, "k_pages", q.dtype)
+    _need(v_pages, "v_pages", q.dtype, k_pages.shape)
+    _need(block_table, "block_table", torch.int32, (B, max_blocks))
+    _need(prefix_lens, "prefix_lens", torch.int32, (B,))
+    if chunk_lens is not None:
+        _need(chunk_lens, "chunk_lens", torch.int32, (B,))
+    n_axes = 1
+    if positions is not None:
+        n_axes = positions.shape[0] if positions.dim() == 3 else 1
+        _need(positions, "positions", torch.int32, (n_axes, B, C) if positions.dim() == 3 else (B, C))
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32)
+        rot = 2 * inv_freq.numel()
+    if pair_axis is not None:
+        _need(pair_axis, "pair_axis", torch.int32, (rot // 2,))
+    for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _need(t, n, q.dtype, (D,))
+    if out is None:
+        out = torch.empty((B, C, Hq, D), dtype=q.dtype, device=q.device)
+    _need(out, "out", q.dtype, (B, C, Hq, D))
+    st = lib.attn_qk_norm_rope_append(_ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(q_norm), _ptr(k_norm), float(eps),
+                                      _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(positions), n_axes,
+                                      _ptr(pair_axis), _ptr(block_table), _ptr(prefix_lens), _ptr(chunk_lens),
+                                      _ptr(out), _ptr(k_pages), _ptr(v_pages), B, C, max_blocks, num_pages, Hq, Hkv,
+                                      D, P, _dt(q), _ptr(err_flag), _stream(stream))
+    _check(st, "attn_qk_norm_rope_append")
+    return out
+
+
+# --------------------------------------------------------------------------- accumulated weights, eviction
+
+def decode_weights_workspace_size(batch, max_blocks, n_qo_heads, n_kv_heads, head_dim, page_size,
+                                  num_splits=0, dtype=PKV_BF16) -> int:
+    n = lib.attn_decode_weights_workspace_size(batch, max_blocks, n_qo_heads, n_kv_heads, head_dim,
+                                               page_size, num_splits, dtype)
+    if n == ctypes.c_size_t(-1).value:
+        raise AttnError(PKV_ERR_INVALID_ARG, "attn_decode_weights_workspace_size")
+    return n
+
+
+def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums, scale, sums_out=None, decay=1.0,
+                         num_splits=0, out=None, lse=None, workspace=None, err_flag=None, stream=None):
+    """Paged decode that adds each key's attention weight to ``weight_sums``
+    ``[B, Hkv, max_blocks * page_size]`` (in place, or into ``sums_out``), through
+    ``attn_decode_paged_weights``. Returns ``(out, lse, sums)``."""
+    B, Hq, D = q.shape
+    num_pages, Hkv, P, D2 = k_pages.shape
+    assert D2 == D
+    max_blocks = block_table.shape[1]
+    _need(q, "q")
+    _here(q, "q")
+    _need(k_pages, "k_pages", q.dtype)
+    _need(v_pages, "v_pages", q.dtype, k_pages.shape)
+    _need(block_table, "block_table", torch.int32, (B, max_blocks))
+    _need(kv_lens, "kv_lens", torch.int32, (B,))
+    _need(weight_sums, "weight_sums", torch.float32, (B, Hkv, max_blocks * P))
+    if sums_out is None:
+        sums_out = weight_sums
+    _need(sums_out, "sums_out", torch.float32, weight_sums.shape)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = alloc_workspace(decode_weights_workspace_size(B, max_blocks, Hq, Hkv, D, P, num_splits, _dt(q)),
+                                    q.device)
+    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.attn_decode_paged_weights(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(kv_lens),
+                                       _ptr(out), _ptr(lse), _ptr(weight_sums), _ptr(sums_out), B, max_blocks,
+                                       num_pages, Hq, Hkv, D, P, float(scale), float(decay), int(num_splits), _dt(q),
+                                       _ptr(workspace), wsz, _ptr(err_flag), _stream(stream))
+    _check(st, "attn_decode_paged_weights")
+    return out, lse, sums_out
+
+
+def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_table, budget, n_sink=0, n_recent=0,
+                kept=None, new_lens=None, new_sums=None, err_flag=None, stream=None):
+    """Cuts every sequence to ``budget`` tokens per KV head, moved to the pages of
+    ``new_block_table``, through ``attn_cache_evict``. Returns ``(kept, new_lens, new_sums)``."""
+    num_pages, Hkv, P, D = k_pages.shape
+    B, max_blocks = block_table.shape
+    new_blocks = new_block_table.shape[1]
+    _need(k_pages, "k_pages")
+    _here(k_pages, "k_pages")
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
+    _need(block_table, "block_table", torch.int32)
+    _need(kv_lens, "kv_lens", torch.int32, (B,))
+    _need(weight_sums, "weight_sums", torch.float32, (B, Hkv, max_blocks * P))
+    _need(new_block_table, "new_block_table", torch.int32, (B, new_blocks))
+    budget = int(budget)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=k_pages.device)
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=k_pages.device)
+    if new_sums is None:
+        new_sums = torch.empty((B, Hkv, new_blocks * P), dtype=torch.float32, device=k_pages.device)
+    _need(kept, "kept", torch.int32, (B, Hkv, budget))
+    _need(new_lens, "new_lens", torch.int32, (B,))
+    _need(new_sums, "new_sums", torch.float32, (B, Hkv, new_blocks * P))
+    st = lib.attn_cache_evict(_ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(kv_lens), _ptr(weight_sums),
+                              _ptr(new_block_table), _ptr(kept), _ptr(new_lens), _ptr(new_sums), B, max_blocks,
+                              new_blocks, num_pages, Hkv, D, P, budget, int(n_sink), int(n_recent), _dt(k_pages),
+                              _ptr(err_flag), _stream(stream))
+    _check(st, "attn_cache_evict")
+    return kept, new_lens, new_sums
 
 
 def debug_decode_stall(page: int, wait_limit_ns: int = 0) -> None:

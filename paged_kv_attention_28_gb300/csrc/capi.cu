@@ -149,8 +149,21 @@ struct DecodeCall {
   const float* v_scale = nullptr;
 };
 
+// The accumulated weights of a decode call.
+struct WeightsCall {
+  const float* sums_in;
+  float* sums_out;
+  float decay;
+};
+
+// Scratch behind the split partials: the logits, then the log-sum-exps.
+static size_t decode_weights_extra_bytes(int batch, int max_blocks, int n_qo_heads, int page_size) {
+  const size_t rows = (size_t)batch * n_qo_heads;
+  return align_up(rows * max_blocks * page_size * sizeof(float), 256) + align_up(rows * sizeof(float), 256);
+}
+
 static int decode_common(const DecodeCall& c, bool unified, float phi, int32_t* fallback_count,
-                         bool fp8 = false) {
+                         bool fp8 = false, const WeightsCall* weights = nullptr) {
   if (c.batch < 0 || c.max_blocks < 1 || c.num_pages < 1 || c.n_qo_heads < 1 ||
       c.n_kv_heads < 1 || c.head_dim < 1 || c.page_size < 1 || c.num_splits < 0)
     return PKV_ERR_INVALID_ARG;
@@ -169,7 +182,8 @@ static int decode_common(const DecodeCall& c, bool unified, float phi, int32_t* 
   if (fp8 && c.n_kv_heads % 2) return PKV_ERR_UNSUPPORTED;  // two KV heads per CTA
   const SplitPlan plan = plan_decode(c.batch, c.max_blocks, c.n_qo_heads, c.n_kv_heads, c.head_dim, c.page_size,
                                      c.num_splits, fp8 ? PKV_FP8_E4M3 : c.dtype);
-  const size_t need = decode_ws_bytes(c.batch, c.n_qo_heads, c.n_kv_heads, c.head_dim, plan.num_splits);
+  const size_t part = decode_ws_bytes(c.batch, c.n_qo_heads, c.n_kv_heads, c.head_dim, plan.num_splits);
+  const size_t need = part + (weights ? decode_weights_extra_bytes(c.batch, c.max_blocks, c.n_qo_heads, c.page_size) : 0);
   if (need > 0 && (!c.workspace || c.workspace_bytes < need ||
                    (reinterpret_cast<uintptr_t>(c.workspace) & 255u) != 0))
     return PKV_ERR_WORKSPACE;
@@ -185,7 +199,7 @@ static int decode_common(const DecodeCall& c, bool unified, float phi, int32_t* 
   a.out = c.out;
   a.lse = c.lse;
   const size_t rows = (size_t)c.batch * c.n_qo_heads;
-  if (need > 0) {
+  if (part > 0) {
     char* w = static_cast<char*>(c.workspace);
     a.part_o = reinterpret_cast<float*>(w);
     w += align_up(rows * plan.num_splits * c.head_dim * sizeof(float), 256);
@@ -210,6 +224,12 @@ static int decode_common(const DecodeCall& c, bool unified, float phi, int32_t* 
   a.fp8 = fp8;
   a.k_scale = c.k_scale;
   a.v_scale = c.v_scale;
+  if (weights) {
+    a.logits = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + part);
+    if (!a.lse)
+      a.lse = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + need - align_up(rows * sizeof(float), 256));
+    return launch_decode_weights(DecodeWeightsArgs{a, weights->sums_in, weights->sums_out, weights->decay}, c.stream);
+  }
   return launch_decode(a, c.stream);
 }
 
@@ -426,6 +446,103 @@ int attn_decode_cascade(const void* q, const void* k_pages, const void* v_pages,
   w += align_up(rows * suf.num_splits * head_dim * 4, 256);
   a.suf_lse = reinterpret_cast<float*>(w);
   return launch_cascade(a, static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_decode_weights_workspace_size(int batch, int max_blocks_per_seq, int n_qo_heads,
+                                          int n_kv_heads, int head_dim, int page_size,
+                                          int num_splits, int dtype) {
+  if (dtype != PKV_F32 && dtype != PKV_BF16) return (size_t)-1;
+  const size_t part = attn_decode_workspace_size(batch, max_blocks_per_seq, n_qo_heads, n_kv_heads, head_dim,
+                                                 page_size, num_splits, dtype);
+  if (part == (size_t)-1) return part;
+  return part + decode_weights_extra_bytes(batch, max_blocks_per_seq, n_qo_heads, page_size);
+}
+
+int attn_decode_paged_weights(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* kv_lens, void* out,
+                              float* lse, const float* sums_in, float* sums_out, int batch,
+                              int max_blocks_per_seq, int num_pages, int n_qo_heads,
+                              int n_kv_heads, int head_dim, int page_size, float scale, float decay,
+                              int num_splits, int dtype, void* workspace, size_t workspace_bytes,
+                              int32_t* err_flag, void* stream) {
+  const pkv::CallRange range("attn_decode_paged_weights");
+  if (!std::isfinite(decay)) return PKV_ERR_INVALID_ARG;
+  if (batch > 0 && (!sums_in || !sums_out || !aligned16(sums_in) || !aligned16(sums_out)))
+    return PKV_ERR_INVALID_ARG;
+  DecodeCall c{q, k_pages, v_pages, block_table, kv_lens, out, lse, batch, max_blocks_per_seq,
+               num_pages, n_qo_heads, n_kv_heads, head_dim, page_size, scale, num_splits, dtype,
+               workspace, workspace_bytes, err_flag, static_cast<cudaStream_t>(stream)};
+  const WeightsCall w{sums_in, sums_out, decay};
+  return decode_common(c, false, 0.0f, nullptr, false, &w);
+}
+
+int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
+                     const int32_t* kv_lens, const float* sums, const int32_t* new_block_table,
+                     int32_t* kept, int32_t* new_lens, float* new_sums, int batch,
+                     int max_blocks_per_seq, int new_max_blocks, int num_pages, int n_kv_heads,
+                     int head_dim, int page_size, int budget, int n_sink, int n_recent, int dtype,
+                     int32_t* err_flag, void* stream) {
+  const pkv::CallRange range("attn_cache_evict");
+  if (batch < 0 || max_blocks_per_seq < 1 || new_max_blocks < 1 || num_pages < 1 || n_kv_heads < 1 ||
+      head_dim < 1 || page_size < 1)
+    return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if ((long)max_blocks_per_seq * page_size > 0x7fffffffL || (long)new_max_blocks * page_size > 0x7fffffffL)
+    return PKV_ERR_INVALID_ARG;
+  if (budget < 1 || budget > new_max_blocks * page_size || n_sink < 0 || n_recent < 0 ||
+      (long)n_sink + n_recent > budget)
+    return PKV_ERR_INVALID_ARG;
+  if (batch == 0) return PKV_OK;
+  if (!k_pages || !v_pages || !block_table || !kv_lens || !sums || !new_block_table || !kept || !new_lens || !new_sums)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return PKV_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128) || page_size != 16) return PKV_ERR_UNSUPPORTED;
+  if (batch > 65535 || n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  EvictArgs a{k_pages, v_pages, block_table, kv_lens, sums, new_block_table, kept, new_lens, new_sums, batch,
+              max_blocks_per_seq, new_max_blocks, num_pages, n_kv_heads, head_dim, page_size, budget, n_sink,
+              n_recent, dtype, err_flag};
+  return launch_evict(a, static_cast<cudaStream_t>(stream));
+}
+
+int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const void* q_norm,
+                             const void* k_norm, float norm_eps, const float* inv_freq,
+                             int rotary_dim, int interleaved, const int32_t* positions, int n_axes,
+                             const int32_t* pair_axis, const int32_t* block_table,
+                             const int32_t* prefix_lens, const int32_t* chunk_lens, void* q_out,
+                             void* k_pages, void* v_pages, int batch, int chunk_len,
+                             int max_blocks_per_seq, int num_pages, int n_qo_heads, int n_kv_heads,
+                             int head_dim, int page_size, int dtype, int32_t* err_flag,
+                             void* stream) {
+  const pkv::CallRange range("attn_qk_norm_rope_append");
+  if (batch < 0 || chunk_len < 0 || max_blocks_per_seq < 1 || num_pages < 1 || n_qo_heads < 1 ||
+      n_kv_heads < 1 || head_dim < 1 || page_size < 1)
+    return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if ((long)max_blocks_per_seq * page_size > 0x7fffffffL) return PKV_ERR_INVALID_ARG;
+  if (rotary_dim < 0 || rotary_dim > head_dim || n_axes < 1 || (interleaved != 0 && interleaved != 1))
+    return PKV_ERR_INVALID_ARG;
+  if ((q_norm || k_norm) && !(norm_eps >= 0.0f && std::isfinite(norm_eps))) return PKV_ERR_INVALID_ARG;
+  if (batch == 0 || chunk_len == 0) return PKV_OK;
+  if (!q || !k || !v || !block_table || !prefix_lens || !q_out || !k_pages || !v_pages) return PKV_ERR_INVALID_ARG;
+  if (rotary_dim > 0 && !inv_freq) return PKV_ERR_INVALID_ARG;
+  const int64_t qw = (int64_t)n_qo_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
+  if (q_stride < qw || k_stride < kw || v_stride < kw) return PKV_ERR_INVALID_ARG;
+  if (q_stride % 4 || k_stride % 4 || v_stride % 4) return PKV_ERR_INVALID_ARG;
+  if (q_out == q && q_stride != qw) return PKV_ERR_INVALID_ARG;
+  const uintptr_t quad = dtype == PKV_F32 ? 16 : 8;
+  for (const void* p : {q, k, v, q_norm, k_norm, static_cast<const void*>(q_out)})
+    if (reinterpret_cast<uintptr_t>(p) % quad) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return PKV_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128) || page_size != 16 || rotary_dim % 8 || n_axes > 4)
+    return PKV_ERR_UNSUPPORTED;
+  if ((int64_t)batch * chunk_len > 0x7fffffffL || n_qo_heads > (1 << 20) || n_kv_heads > (1 << 20))
+    return PKV_ERR_UNSUPPORTED;
+  AppendArgs a{q, k, v, q_stride, k_stride, v_stride, q_norm, k_norm, norm_eps, inv_freq, rotary_dim,
+               interleaved, positions, n_axes, pair_axis, block_table, prefix_lens, chunk_lens, q_out,
+               k_pages, v_pages, batch, chunk_len, max_blocks_per_seq, num_pages, n_qo_heads, n_kv_heads,
+               head_dim, page_size, dtype, err_flag};
+  return launch_append(a, static_cast<cudaStream_t>(stream));
 }
 
 int attn_debug_decode_stall(int page, unsigned long long wait_limit_ns) {

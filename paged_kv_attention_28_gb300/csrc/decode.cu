@@ -64,6 +64,7 @@ int launch_merge_splits(const DecodeArgs& a, cudaStream_t stream) {
 
 int dispatch_decode_unified(const DecodeArgs& a, cudaStream_t stream);  // decode_um.cu
 int dispatch_decode_fp8(const DecodeArgs& a, cudaStream_t stream);      // decode_fp8.cu
+int dispatch_decode_logits(const DecodeArgs& a, cudaStream_t stream);   // decode_weights.cu
 
 int decode_ctas_per_sm(int dtype, int head_dim, int group) {
 #define PKV_CPS(TT, F8)                                                        \
@@ -103,6 +104,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   const int rc = decode_tc_supported(a) ? launch_decode_tc(a, stream)
                  : a.fp8                  ? dispatch_decode_fp8(a, stream)
                  : a.unified              ? dispatch_decode_unified(a, stream)
+                 : a.logits               ? dispatch_decode_logits(a, stream)
                                           : dispatch_decode<false>(a, stream);
   if (rc != PKV_OK) return rc;
   if (a.num_splits > 1) return launch_merge_splits(a, stream);

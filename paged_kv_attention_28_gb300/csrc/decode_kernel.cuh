@@ -270,7 +270,9 @@ __device__ void write_group_const(const DecodeArgs& a, int b, int g, float o, fl
   }
 }
 
-template <typename T, int D, int P, int G, bool UNIFIED, bool FP8 = false>
+// LOGITS: every key's logits, in base-2 units, also go to a.logits [batch][n_qo_heads][max_blocks
+// * P] in fp32 (the weights that each key received need the final lse and are formed after it).
+template <typename T, int D, int P, int G, bool UNIFIED, bool FP8 = false, bool LOGITS = false>
 __global__ void __launch_bounds__(DecodeCfg<T, D, P, G, UNIFIED, FP8>::THREADS,
                                   DecodeCfg<T, D, P, G, UNIFIED, FP8>::MIN_BLOCKS)
 decode_paged_kernel(const DecodeArgs a) {
@@ -537,6 +539,11 @@ decode_paged_kernel(const DecodeArgs a) {
             so[it] = reduce_scatter_heads<G, C::LPT>(sc[it], j);
             const int t = (ch * C::NIT + it) * C::TPI + tg;
             if (t >= valid) so[it] = -INFINITY;
+            if constexpr (LOGITS) {
+              if (t < valid && j % LPH == 0)
+                a.logits[((size_t)b * a.n_qo_heads + g * G + h_own) * ((size_t)a.max_blocks * P) +
+                         (size_t)(first + i) * P + t] = so[it];
+            }
           }
           // this chunk's max of head gi, on every lane (lane gi * LPH owns head gi)
           auto chunk_max = [&](float (&mx)[G]) {
@@ -647,6 +654,11 @@ decode_paged_kernel(const DecodeArgs a) {
             if (t >= valid) {
 #pragma unroll
               for (int gi = 0; gi < G; ++gi) sc[it][gi] = -INFINITY;
+            }
+            if constexpr (LOGITS) {
+              if (t < valid && j < G)
+                a.logits[((size_t)b * a.n_qo_heads + g * G + j) * ((size_t)a.max_blocks * P) +
+                         (size_t)(first + i) * P + t] = pick<G>(sc[it], j);
             }
           }
 
@@ -864,10 +876,10 @@ decode_paged_kernel(const DecodeArgs a) {
   }
 }
 
-template <typename T, int D, int P, int G, bool UNIFIED, bool FP8 = false>
+template <typename T, int D, int P, int G, bool UNIFIED, bool FP8 = false, bool LOGITS = false>
 int launch_decode_t(const DecodeArgs& a, cudaStream_t stream) {
   using C = DecodeCfg<T, D, P, G, UNIFIED, FP8>;
-  auto kern = decode_paged_kernel<T, D, P, G, UNIFIED, FP8>;
+  auto kern = decode_paged_kernel<T, D, P, G, UNIFIED, FP8, LOGITS>;
   static FuncConfigured configured;
   if (!configured.ensure(reinterpret_cast<const void*>(kern), C::SMEM)) return PKV_ERR_LAUNCH;
   dim3 grid(a.num_splits, a.n_kv_heads / C::HPC, a.batch);
@@ -882,12 +894,12 @@ constexpr int ctas_per_sm_t() {
   return by_smem < C::MIN_BLOCKS ? by_smem : C::MIN_BLOCKS;
 }
 
-template <bool UNIFIED>
+template <bool UNIFIED, bool LOGITS = false>
 int dispatch_decode(const DecodeArgs& a, cudaStream_t stream) {
   const int G = a.n_qo_heads / a.n_kv_heads;
 #define PKV_DEC_CASE(TT, DD, GG)                                   \
   if (a.head_dim == DD && G == GG)                                 \
-    return launch_decode_t<TT, DD, 16, GG, UNIFIED>(a, stream);
+    return launch_decode_t<TT, DD, 16, GG, UNIFIED, false, LOGITS>(a, stream);
 #define PKV_DEC_DT(TT)                                             \
   PKV_DEC_CASE(TT, 64, 1) PKV_DEC_CASE(TT, 64, 2) PKV_DEC_CASE(TT, 64, 4) PKV_DEC_CASE(TT, 64, 8) \
   PKV_DEC_CASE(TT, 128, 1) PKV_DEC_CASE(TT, 128, 2)

@@ -560,7 +560,10 @@ __device__ __forceinline__ void convert_fp8(const DecodeArgs& a, unsigned char* 
 // FP8: the pools hold E4M3 codes with per-(page, KV head) scales; the producers bring a tile of
 // codes into a staging ring and convert it (exactly) to f16 in the K or V ring, q is taken to
 // f16 after a per-row power-of-two scaling, and both products take f16 operands.
-template <int G, bool UNIFIED, bool CASCADE, bool FP8>
+//
+// LOGITS: every key's logits, in base-2 units, also go to a.logits [batch][n_qo_heads][max_blocks
+// * 16] in fp32; 128 keys of a head are one contiguous run of stores by the softmax threads.
+template <int G, bool UNIFIED, bool CASCADE, bool FP8, bool LOGITS = false>
 __global__ void __launch_bounds__(TcL<FP8>::THREADS, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const DecodeArgs a, int n_units) {
@@ -914,6 +917,14 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
           x[h] = t < valid ? __uint_as_float(sr[h]) * (FP8 ? cq[h] * ks : c) : -INFINITY;
           mt[h] = x[h];
         }
+        if constexpr (LOGITS) {
+          if (t < valid) {
+            float* dst = a.logits + ((size_t)u.b * a.n_qo_heads + (size_t)u.hk * G) * ((size_t)a.max_blocks * 16) +
+                         (size_t)(u.first + 8 * j) * 16 + t;
+#pragma unroll
+            for (int h = 0; h < G; ++h) dst[(size_t)h * ((size_t)a.max_blocks * 16)] = x[h];
+          }
+        }
         bool need = false, raise = false;  // the same on every thread
         float alpha[G];
         if constexpr (UNIFIED) {
@@ -1154,7 +1165,7 @@ bool encode_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swz
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int G, bool UNIFIED, bool CASCADE, bool FP8>
+template <int G, bool UNIFIED, bool CASCADE, bool FP8, bool LOGITS = false>
 int launch_tc(const DecodeArgs& a, cudaStream_t stream) {
   using L = TcL<FP8>;
   CUtensorMap mq, mk, mv;
@@ -1181,14 +1192,14 @@ int launch_tc(const DecodeArgs& a, cudaStream_t stream) {
       return check_launch(cudaErrorInvalidValue);
   }
   static FuncConfigured configured;
-  if (!configured.ensure(reinterpret_cast<const void*>(decode_tc_kernel<G, UNIFIED, CASCADE, FP8>), L::SMEM))
+  if (!configured.ensure(reinterpret_cast<const void*>(decode_tc_kernel<G, UNIFIED, CASCADE, FP8, LOGITS>), L::SMEM))
     return PKV_ERR_LAUNCH;
   const long n_units = (long)a.num_splits * a.n_kv_heads * a.batch;
   if (n_units <= 0) return PKV_OK;
   if (n_units > 0x7fffffffL) return PKV_ERR_UNSUPPORTED;
   if (!CASCADE) {
-    decode_tc_kernel<G, UNIFIED, CASCADE, FP8><<<(unsigned)n_units, L::THREADS, L::SMEM, stream>>>(mq, mk, mv, a,
-                                                                                             (int)n_units);
+    decode_tc_kernel<G, UNIFIED, CASCADE, FP8, LOGITS><<<(unsigned)n_units, L::THREADS, L::SMEM, stream>>>(
+        mq, mk, mv, a, (int)n_units);
     return check_launch(cudaGetLastError());
   }
   // cascade: may start while the prefix kernel before it finishes (it waits for that grid
@@ -1203,7 +1214,7 @@ int launch_tc(const DecodeArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, decode_tc_kernel<G, UNIFIED, CASCADE, FP8>, mq, mk, mv, a, (int)n_units));
+  return check_launch(cudaLaunchKernelEx(&cfg, decode_tc_kernel<G, UNIFIED, CASCADE, FP8, LOGITS>, mq, mk, mv, a, (int)n_units));
 }
 
 }  // namespace
@@ -1233,6 +1244,12 @@ int launch_decode_tc(const DecodeArgs& a, cudaStream_t stream) {
     if (a.unified) return PKV_ERR_UNSUPPORTED;
     if (G == 4) return launch_tc<4, false, true, false>(a, stream);
     if (G == 8) return launch_tc<8, false, true, false>(a, stream);
+    return PKV_ERR_UNSUPPORTED;
+  }
+  if (a.logits) {
+    if (a.unified) return PKV_ERR_UNSUPPORTED;
+    if (G == 4) return launch_tc<4, false, false, false, true>(a, stream);
+    if (G == 8) return launch_tc<8, false, false, false, true>(a, stream);
     return PKV_ERR_UNSUPPORTED;
   }
   if (G == 4) return a.unified ? launch_tc<4, true, false, false>(a, stream) : launch_tc<4, false, false, false>(a, stream);

@@ -50,6 +50,9 @@ struct DecodeArgs {
   const float* pre_o = nullptr;
   const float* pre_lse = nullptr;
   int pre_n = 0;
+  // Accumulated weights: where the logits (base-2 units) of every key go, fp32
+  // [batch][n_qo_heads][max_blocks * page_size]; null: not wanted.
+  float* logits = nullptr;
 };
 
 
@@ -171,5 +174,67 @@ int flat_gemm_padded_m(int m);
 FlatGemmPlan plan_flat_gemm(int m, int n, int k);
 int launch_flat_gemm(const FlatGemmArgs& a, cudaStream_t stream);
 int launch_cascade(const CascadeArgs& a, cudaStream_t stream);
+
+// Norm, rotation and page write of new tokens (append.cu); fields as the C call's arguments.
+struct AppendArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const void *q_norm, *k_norm;
+  float eps;
+  const float* inv_freq;
+  int rotary_dim, interleaved;
+  const int32_t* positions;
+  int n_axes;
+  const int32_t *pair_axis, *block_table, *prefix_lens, *chunk_lens;
+  void *q_out, *k_pages, *v_pages;
+  int batch, chunk_len, max_blocks, num_pages, n_qo_heads, n_kv_heads, head_dim, page_size, dtype;
+  int32_t* err_flag;
+};
+int launch_append(const AppendArgs& a, cudaStream_t stream);
+
+// Decode with accumulated weights (decode_weights.cu): the decode with its logits kept in
+// d.logits and its log-sum-exps in d.lse, then sums_out = decay * sums_in + weights.
+struct DecodeWeightsArgs {
+  DecodeArgs d;
+  const float* sums_in;
+  float* sums_out;
+  float decay;
+};
+int launch_decode_weights(const DecodeWeightsArgs& a, cudaStream_t stream);
+
+// Weights that the keys received from a chunk's queries (chunk_weights.cu).
+struct ChunkWeightsArgs {
+  const void *q, *k_pages;
+  const int32_t *block_table, *prefix_lens, *chunk_lens;
+  const float *lse, *sums_in;
+  float* sums_out;
+  int batch, chunk_len, window, max_blocks, num_pages, n_qo_heads, n_kv_heads, head_dim, page_size;
+  float scale, decay;
+  int32_t* err_flag;
+};
+int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream);
+
+// Eviction of the tokens with the least accumulated weight (evict.cu).
+struct EvictArgs {
+  void *k_pages, *v_pages;
+  const int32_t *block_table, *kv_lens;
+  const float* sums;
+  const int32_t* new_block_table;
+  int32_t *kept, *new_lens;
+  float* new_sums;
+  int batch, max_blocks, new_max_blocks, num_pages, n_kv_heads, head_dim, page_size;
+  int budget, n_sink, n_recent, dtype;
+  int32_t* err_flag;
+};
+int launch_evict(const EvictArgs& a, cudaStream_t stream);
+
+// y = act(x w^T + bias) + residual (linear.cu).
+struct LinearArgs {
+  const void *x, *w, *bias, *residual;
+  void* y;
+  int m, n, k, activation;
+  int32_t* err_flag;
+};
+int launch_linear(const LinearArgs& a, cudaStream_t stream);
 
 }  // namespace pkv
