@@ -63,6 +63,13 @@ extern "C" {
 #define PKV_BF16 1
 #define PKV_FP8_E4M3 2 /* page pools of attn_decode_paged_fp8 (planning and workspace queries) */
 
+/* activations of attn_linear */
+#define PKV_ACT_NONE 0
+#define PKV_ACT_RELU 1
+#define PKV_ACT_GELU 2      /* y/2 (1 + erf(y / sqrt 2)) */
+#define PKV_ACT_GELU_TANH 3 /* y/2 (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))) */
+#define PKV_ACT_SILU 4      /* y / (1 + exp(-y)) */
+
 /* status codes */
 #define PKV_OK 0
 #define PKV_ERR_INVALID_ARG (-1) /* null pointer, negative size, inconsistent shape */
@@ -83,7 +90,9 @@ extern "C" {
  *   prefill          : head_dim 128; PKV_BF16; any seq_len >= 1
  *   flat GEMM        : PKV_BF16; 1 <= m <= 64; k a multiple of 8
  *   append           : head_dim 64 or 128; page_size 16; PKV_F32 or PKV_BF16; any head counts
- *   accumulated weights, eviction : as decode (eviction: any head count)
+ *   accumulated weights, eviction : as decode (eviction: any head count); over a chunk as the
+ *                      chunked prefill: PKV_BF16, head_dim 128, page_size 16, groups dividing 128
+ *   linear           : PKV_BF16; any m and n; k a multiple of 8
  */
 
 /* Human-readable name of a status code. Static storage; never NULL. */
@@ -468,6 +477,30 @@ int attn_decode_paged_weights(const void* q, const void* k_pages, const void* v_
                               int32_t* err_flag, void* stream);
 
 /*
+ * The same accumulation for a chunk of queries whose log-sum-exps are known (the lse of
+ * attn_prefill_paged_chunk on the same q, pages, table and prefix_lens):
+ *   sums_out[b][g][t] = decay * sums_in[b][g][t]
+ *                       + sum_{i} sum_{h in group g} exp(scale q_ih . k_t - lse_h(i))
+ * over the queries i >= t - prefix_lens[b] (the causal mask) among the last `window` of the
+ * sequence's new tokens (window 0: all of them), for t < prefix_lens[b] + n; other slots are
+ * neither read nor written. n = chunk_lens[b] where given (0 .. chunk_len; the rest of the
+ * chunk is padding whose q and lse do not matter), else chunk_len.
+ *
+ *   q    : bf16 [batch][chunk_len][n_qo_heads][head_dim]
+ *   lse  : fp32 [batch][n_qo_heads][chunk_len]
+ *   sums : as above; sums_out may be sums_in; q and k_pages 16-byte aligned
+ * A bad length sets PKV_DEVERR_BAD_LEN and leaves the sequence's sums as they were; a bad table
+ * entry sets PKV_DEVERR_BAD_PAGE and makes its keys' sums NaN. bf16, head_dim 128, page_size 16,
+ * groups dividing 128. The product runs on the tcgen05 tensor cores.
+ */
+int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_table,
+                       const int32_t* prefix_lens, const int32_t* chunk_lens, const float* lse,
+                       const float* sums_in, float* sums_out, int batch, int chunk_len, int window,
+                       int max_blocks_per_seq, int num_pages, int n_qo_heads, int n_kv_heads,
+                       int head_dim, int page_size, float scale, float decay, int dtype,
+                       int32_t* err_flag, void* stream);
+
+/*
  * Eviction from the paged cache: every sequence is cut to at most `budget` tokens per KV head.
  * A KV head of a sequence with n = kv_lens[b] > budget tokens keeps the first n_sink, the last
  * n_recent and, of those between, the budget - n_sink - n_recent with the largest sums (equal
@@ -498,6 +531,22 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
                      int max_blocks_per_seq, int new_max_blocks, int num_pages, int n_kv_heads,
                      int head_dim, int page_size, int budget, int n_sink, int n_recent, int dtype,
                      int32_t* err_flag, void* stream);
+
+/*
+ * Linear layer with its epilogue: y = act(x w^T + bias) + residual, for any number of tokens:
+ * the projections on either side of the attention, with what follows them in the same pass.
+ *
+ *   x : bf16 [m][k];  w : bf16 [n][k] (16-byte aligned both)
+ *   bias : bf16 [n], or NULL;  residual : bf16 [m][n], or NULL (2-byte aligned both)
+ *   activation : PKV_ACT_*
+ *   y : bf16 [m][n]; may be residual itself, and must not overlap an input otherwise
+ * The product accumulates in fp32; bias, activation and residual are applied in fp32 and the
+ * result is rounded once. k >= 1 a multiple of 8. m = 0 or n = 0 does nothing. err_flag
+ * (nullable) gets PKV_DEVERR_TIMEOUT if a bounded wait gave up; the outputs affected are NaN.
+ * Up to 64 tokens run as attn_flat_gemm does, more on a tiled kernel.
+ */
+int attn_linear(const void* x, const void* w, const void* bias, const void* residual, void* y,
+                int m, int n, int k, int activation, int dtype, int32_t* err_flag, void* stream);
 
 /*
  * Failure-handling hook for tests (the pages have no counterpart). It lets a test make a

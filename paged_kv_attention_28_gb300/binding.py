@@ -37,7 +37,7 @@ EXPORTS = [
     "attn_decode_paged_noalloc", "attn_decode_paged_fp8", "attn_prefill_paged_chunk",
     "attn_flat_gemm", "attn_flat_gemm_num_splits", "attn_debug_decode_stall",
     "attn_qk_norm_rope_append", "attn_decode_weights_workspace_size", "attn_decode_paged_weights",
-    "attn_cache_evict",
+    "attn_cache_evict", "attn_chunk_weights", "attn_linear",
 ]
 
 
@@ -97,6 +97,10 @@ def _load() -> ctypes.CDLL:
     lib.attn_decode_paged_weights.argtypes = [vp] * 9 + [i32] * 7 + [f32, f32, i32, i32, vp, sz, vp, vp]
     lib.attn_cache_evict.restype = i32
     lib.attn_cache_evict.argtypes = [vp] * 9 + [i32] * 11 + [vp, vp]
+    lib.attn_chunk_weights.restype = i32
+    lib.attn_chunk_weights.argtypes = [vp] * 8 + [i32] * 9 + [f32, f32, i32, vp, vp]
+    lib.attn_linear.restype = i32
+    lib.attn_linear.argtypes = [vp] * 5 + [i32] * 5 + [vp, vp]
     lib.attn_debug_decode_stall.restype = i32
     lib.attn_debug_decode_stall.argtypes = [i32, ctypes.c_ulonglong]
     lib.attn_flat_gemm_num_splits.restype = i32
@@ -484,6 +488,34 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums,
     return out, lse, sums_out
 
 
+def chunk_weights(q, k_pages, block_table, prefix_lens, lse, weight_sums, scale, sums_out=None, decay=1.0, window=0,
+                  chunk_lens=None, err_flag=None, stream=None):
+    """Adds the attention weight that every key receives from a chunk's queries (the last
+    ``window`` of them; 0: all) to ``weight_sums`` (in place, or into ``sums_out``), through
+    ``attn_chunk_weights``. ``lse`` ``[B, Hq, C]`` is ``prefill_paged_chunk``'s. Returns the sums."""
+    B, C, Hq, D = q.shape
+    num_pages, Hkv, P, D2 = k_pages.shape
+    assert D2 == D
+    max_blocks = block_table.shape[1]
+    _need(q, "q")
+    _here(q, "q")
+    _need(k_pages, "k_pages", q.dtype)
+    _need(block_table, "block_table", torch.int32, (B, max_blocks))
+    _need(prefix_lens, "prefix_lens", torch.int32, (B,))
+    if chunk_lens is not None:
+        _need(chunk_lens, "chunk_lens", torch.int32, (B,))
+    _need(lse, "lse", torch.float32, (B, Hq, C))
+    _need(weight_sums, "weight_sums", torch.float32, (B, Hkv, max_blocks * P))
+    if sums_out is None:
+        sums_out = weight_sums
+    _need(sums_out, "sums_out", torch.float32, weight_sums.shape)
+    st = lib.attn_chunk_weights(_ptr(q), _ptr(k_pages), _ptr(block_table), _ptr(prefix_lens), _ptr(chunk_lens),
+                                _ptr(lse), _ptr(weight_sums), _ptr(sums_out), B, C, int(window), max_blocks, num_pages,
+                                Hq, Hkv, D, P, float(scale), float(decay), _dt(q), _ptr(err_flag), _stream(stream))
+    _check(st, "attn_chunk_weights")
+    return sums_out
+
+
 def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_table, budget, n_sink=0, n_recent=0,
                 kept=None, new_lens=None, new_sums=None, err_flag=None, stream=None):
     """Cuts every sequence to ``budget`` tokens per KV head, moved to the pages of
@@ -514,6 +546,34 @@ def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_t
                               _ptr(err_flag), _stream(stream))
     _check(st, "attn_cache_evict")
     return kept, new_lens, new_sums
+
+
+# --------------------------------------------------------------------------- linear
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def linear(x, w, bias=None, activation="none", residual=None, out=None, err_flag=None, stream=None):
+    """``act(x w^T + bias) + residual`` through ``attn_linear``: ``x`` ``[m, k]``, ``w`` ``[n, k]``,
+    bf16; ``activation`` one of ``ACTIVATIONS``. ``out`` may be ``residual``."""
+    m, k = x.shape
+    n = w.shape[0]
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}, one of {sorted(ACTIVATIONS)}")
+    _need(x, "x")
+    _here(x, "x")
+    _need(w, "w", x.dtype, (n, k))
+    if bias is not None:
+        _need(bias, "bias", x.dtype, (n,))
+    if residual is not None:
+        _need(residual, "residual", x.dtype, (m, n))
+    if out is None:
+        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    _need(out, "out", x.dtype, (m, n))
+    st = lib.attn_linear(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(out), m, n, k, ACTIVATIONS[activation],
+                         _dt(x), _ptr(err_flag), _stream(stream))
+    _check(st, "attn_linear")
+    return out
 
 
 def debug_decode_stall(page: int, wait_limit_ns: int = 0) -> None:

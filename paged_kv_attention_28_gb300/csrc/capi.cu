@@ -476,6 +476,47 @@ int attn_decode_paged_weights(const void* q, const void* k_pages, const void* v_
   return decode_common(c, false, 0.0f, nullptr, false, &w);
 }
 
+int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_table,
+                       const int32_t* prefix_lens, const int32_t* chunk_lens, const float* lse,
+                       const float* sums_in, float* sums_out, int batch, int chunk_len, int window,
+                       int max_blocks_per_seq, int num_pages, int n_qo_heads, int n_kv_heads,
+                       int head_dim, int page_size, float scale, float decay, int dtype,
+                       int32_t* err_flag, void* stream) {
+  const pkv::CallRange range("attn_chunk_weights");
+  if (batch < 0 || chunk_len < 0 || window < 0 || max_blocks_per_seq < 1 || num_pages < 1 || n_qo_heads < 1 ||
+      n_kv_heads < 1 || head_dim < 1 || page_size < 1)
+    return PKV_ERR_INVALID_ARG;
+  if (n_qo_heads % n_kv_heads || !std::isfinite(scale) || !std::isfinite(decay)) return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if ((long)max_blocks_per_seq * page_size > 0x7fffffffL) return PKV_ERR_INVALID_ARG;
+  if (chunk_len > max_blocks_per_seq * page_size) return PKV_ERR_INVALID_ARG;
+  if (batch == 0 || chunk_len == 0) return PKV_OK;
+  if (!q || !k_pages || !block_table || !prefix_lens || !lse || !sums_in || !sums_out) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pages)) return PKV_ERR_INVALID_ARG;
+  const int G = n_qo_heads / n_kv_heads;
+  if (dtype != PKV_BF16 || head_dim != 128 || page_size != 16 || 128 % G) return PKV_ERR_UNSUPPORTED;
+  ChunkWeightsArgs a{q, k_pages, block_table, prefix_lens, chunk_lens, lse, sums_in, sums_out, batch, chunk_len,
+                     window, max_blocks_per_seq, num_pages, n_qo_heads, n_kv_heads, head_dim, page_size, scale,
+                     decay, err_flag};
+  return launch_chunk_weights(a, static_cast<cudaStream_t>(stream));
+}
+
+int attn_linear(const void* x, const void* w, const void* bias, const void* residual, void* y,
+                int m, int n, int k, int activation, int dtype, int32_t* err_flag, void* stream) {
+  const pkv::CallRange range("attn_linear");
+  if (m < 0 || n < 0 || k < 1) return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
+  if (activation < PKV_ACT_NONE || activation > PKV_ACT_SILU) return PKV_ERR_INVALID_ARG;
+  if (m == 0 || n == 0) return PKV_OK;
+  if (!x || !w || !y) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w)) return PKV_ERR_INVALID_ARG;
+  for (const void* p : {bias, residual, static_cast<const void*>(y)})
+    if (reinterpret_cast<uintptr_t>(p) & 1) return PKV_ERR_INVALID_ARG;
+  if (dtype != PKV_BF16 || k % 8) return PKV_ERR_UNSUPPORTED;
+  return launch_linear(LinearArgs{x, w, bias, residual, y, m, n, k, activation, err_flag},
+                       static_cast<cudaStream_t>(stream));
+}
+
 int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
                      const int32_t* kv_lens, const float* sums, const int32_t* new_block_table,
                      int32_t* kept, int32_t* new_lens, float* new_sums, int batch,

@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include "epilogue.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -66,6 +67,7 @@ struct FgArgs {
   int m, n, k;
   int kc_per_cta;    // 64-wide K slices per CTA of a cluster
   int n_kc;          // 64-wide K slices in all
+  Epilogue ep;       // EPI instantiations only
 };
 
 struct FgMisc {
@@ -111,7 +113,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 // Grid (S, tiles): CTA (r, t) multiplies K slices [r * kc_per_cta, ...) of W tile t, and
 // the S CTAs of tile t form one cluster. Every thread reaches both cluster barriers on
 // every path: the mbarrier waits are bounded, and a failed one only marks the result.
-template <int NP>
+// EPI: every sum goes through bias, activation and residual before it is stored.
+template <int NP, bool EPI>
 __global__ void __launch_bounds__(FG_THREADS)
 flat_gemm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                  const FgArgs a) {
@@ -253,13 +256,29 @@ flat_gemm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
     for (int i = 0; i < NP; ++i) acc[i] = NAN;
   }
   const int n0 = tile * FG_BM;
+  // N sums of feature n, tokens m0 ..: epilogue and store
+  auto emit = [&](auto& v, int m0, int n) {
+    constexpr int N = sizeof(v) / sizeof(float);
+    if constexpr (EPI) {
+      if (a.ep.bias) {
+        const float b = __bfloat162float(a.ep.bias[n]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += b;
+      }
+      activate_all(v, a.ep.activation);
+      if (a.ep.residual) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (m0 + i < a.m) v[i] += __bfloat162float(a.ep.residual[(size_t)(m0 + i) * a.n + n]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (m0 + i < a.m) a.y[(size_t)(m0 + i) * a.n + n] = __float2bfloat16_rn(v[i]);
+  };
   if (S == 1) {
     const int n = n0 + row;
-    if (n < a.n) {
-#pragma unroll
-      for (int m = 0; m < NP; ++m)
-        if (m < a.m) a.y[(size_t)m * a.n + n] = __float2bfloat16_rn(acc[m]);
-    }
+    if (n < a.n) emit(acc, 0, n);
   } else {
     // Partial tile into this CTA's reduction buffer (the ring is idle: every copy has
     // landed and every product has read it), then CTA r sums rows r, r + S, ... over
@@ -286,10 +305,8 @@ flat_gemm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
       }
       const int n = n0 + rr;
       if (n < a.n) {
-        const float vals[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (m0 + j < a.m) a.y[(size_t)(m0 + j) * a.n + n] = __float2bfloat16_rn(vals[j]);
+        float vals[4] = {sum.x, sum.y, sum.z, sum.w};
+        emit(vals, m0, n);
       }
     }
     __syncwarp();
@@ -315,8 +332,8 @@ bool encode_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t ou
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NP>
-int launch_fg(const FlatGemmArgs& p, const FlatGemmPlan& plan, cudaStream_t stream) {
+template <int NP, bool EPI>
+int launch_fg(const FlatGemmArgs& p, const Epilogue& ep, const FlatGemmPlan& plan, cudaStream_t stream) {
   using C = FgCfg<NP>;
   CUtensorMap mw, mx;
   // W [N][K]: boxes of 128 rows x 64 columns; X [M][K]: NP rows (rows past M read as 0)
@@ -324,8 +341,8 @@ int launch_fg(const FlatGemmArgs& p, const FlatGemmPlan& plan, cudaStream_t stre
       !encode_bf16_2d(&mx, p.x, (uint64_t)p.k, (uint64_t)p.m, NP))
     return check_launch(cudaErrorInvalidValue);
   static FuncConfigured configured;
-  if (!configured.ensure(reinterpret_cast<const void*>(flat_gemm_kernel<NP>), C::SMEM)) return PKV_ERR_LAUNCH;
-  FgArgs a{static_cast<__nv_bfloat16*>(p.y), p.err_flag, p.m, p.n, p.k, plan.kc_per_cta, plan.n_kc};
+  if (!configured.ensure(reinterpret_cast<const void*>(flat_gemm_kernel<NP, EPI>), C::SMEM)) return PKV_ERR_LAUNCH;
+  FgArgs a{static_cast<__nv_bfloat16*>(p.y), p.err_flag, p.m, p.n, p.k, plan.kc_per_cta, plan.n_kc, ep};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)plan.splits, (unsigned)plan.tiles, 1);
   cfg.blockDim = dim3(FG_THREADS, 1, 1);
@@ -338,7 +355,18 @@ int launch_fg(const FlatGemmArgs& p, const FlatGemmPlan& plan, cudaStream_t stre
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, flat_gemm_kernel<NP>, mw, mx, a));
+  return check_launch(cudaLaunchKernelEx(&cfg, flat_gemm_kernel<NP, EPI>, mw, mx, a));
+}
+
+template <bool EPI>
+int launch_fg_any(const FlatGemmArgs& a, const Epilogue& ep, cudaStream_t stream) {
+  const FlatGemmPlan plan = plan_flat_gemm(a.m, a.n, a.k);
+  if (plan.tiles > 65535) return PKV_ERR_UNSUPPORTED;
+  switch (flat_gemm_padded_m(a.m)) {
+    case 16: return launch_fg<16, EPI>(a, ep, plan, stream);
+    case 32: return launch_fg<32, EPI>(a, ep, plan, stream);
+    default: return launch_fg<64, EPI>(a, ep, plan, stream);
+  }
 }
 
 }  // namespace
@@ -369,13 +397,12 @@ FlatGemmPlan plan_flat_gemm(int m, int n, int k) {
 }
 
 int launch_flat_gemm(const FlatGemmArgs& a, cudaStream_t stream) {
-  const FlatGemmPlan plan = plan_flat_gemm(a.m, a.n, a.k);
-  if (plan.tiles > 65535) return PKV_ERR_UNSUPPORTED;
-  switch (flat_gemm_padded_m(a.m)) {
-    case 16: return launch_fg<16>(a, plan, stream);
-    case 32: return launch_fg<32>(a, plan, stream);
-    default: return launch_fg<64>(a, plan, stream);
-  }
+  return launch_fg_any<false>(a, Epilogue{}, stream);
+}
+
+int launch_flat_linear(const LinearArgs& a, cudaStream_t stream) {
+  const Epilogue ep{static_cast<const __nv_bfloat16*>(a.bias), static_cast<const __nv_bfloat16*>(a.residual), a.activation};
+  return launch_fg_any<true>(FlatGemmArgs{a.x, a.w, a.y, a.err_flag, a.m, a.n, a.k}, ep, stream);
 }
 
 }  // namespace pkv

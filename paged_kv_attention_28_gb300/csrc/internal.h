@@ -236,5 +236,7 @@ struct LinearArgs {
   int32_t* err_flag;
 };
 int launch_linear(const LinearArgs& a, cudaStream_t stream);
+// The same for m <= kFlatGemmMaxM, on the flat GEMM's kernel (flat_gemm.cu).
+int launch_flat_linear(const LinearArgs& a, cudaStream_t stream);
 
 }  // namespace pkv

@@ -144,6 +144,40 @@ def test_evict_refuses(b, bad, want):
     assert b.lib.attn_cache_evict(*evict_args(b, **bad)) == want
 
 
+def chunk_args(b, **kw):
+    a = dict(q=P, kp=P, bt=P, pl=P, cl=None, lse=P, si=P, so=P, batch=1, chunk=8, window=0, mb=4, np=4, hq=8, hkv=2,
+             d=128, page=16, scale=0.1, decay=1.0, dt=b.PKV_BF16)
+    a.update(kw)
+    return list(a.values()) + [None, None]
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(q=None), -1), (dict(lse=None), -1), (dict(si=None), -1), (dict(so=None), -1), (dict(kp=None), -1),
+    (dict(q=ODD), -1), (dict(kp=ODD), -1), (dict(window=-1), -1), (dict(chunk=-1), -1), (dict(chunk=65), -1),
+    (dict(scale=float("inf")), -1), (dict(decay=float("nan")), -1), (dict(hq=9), -1), (dict(dt=7), -1), (dict(mb=0), -1),
+    (dict(dt=0), -2), (dict(d=64), -2), (dict(page=8, mb=8), -2), (dict(hq=6), -2), (dict(batch=0, q=None), 0),
+    (dict(chunk=0, q=None), 0),
+])
+def test_chunk_weights_refuses(b, bad, want):
+    assert b.lib.attn_chunk_weights(*chunk_args(b, **bad)) == want
+
+
+def linear_args(b, **kw):
+    a = dict(x=P, w=P, bias=None, res=None, y=P, m=4, n=8, k=64, act=0, dt=b.PKV_BF16)
+    a.update(kw)
+    return list(a.values()) + [None, None]
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(x=ODD), -1), (dict(w=ODD), -1), (dict(m=-1), -1),
+    (dict(n=-1), -1), (dict(k=0), -1), (dict(act=5), -1), (dict(act=-1), -1), (dict(dt=3), -1),
+    (dict(y=ctypes.c_void_p((1 << 20) + 1)), -1), (dict(bias=ctypes.c_void_p((1 << 20) + 1)), -1),
+    (dict(k=12), -2), (dict(dt=0), -2), (dict(m=0, x=None), 0), (dict(n=0, w=None), 0),
+])
+def test_linear_refuses(b, bad, want):
+    assert b.lib.attn_linear(*linear_args(b, **bad)) == want
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(b):
     q = torch.zeros(1, 1, 8, 64)
     kp = torch.zeros(4, 2, 16, 64)
@@ -153,5 +187,11 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(b):
         b.qk_norm_rope_append(q, q[:, :, :2], q[:, :, :2], kp, kp, i, n)
     with pytest.raises(ValueError):
         b.decode_paged_weights(q[:, 0], kp, kp, i, n, torch.zeros(1, 2, 64), 0.1)
+    with pytest.raises(ValueError):
+        b.chunk_weights(q, kp, i, n, torch.zeros(1, 8, 1), torch.zeros(1, 2, 64), 0.1)
+    with pytest.raises(ValueError):
+        b.linear(q[0, 0], q[0, 0])
+    with pytest.raises(ValueError):
+        b.linear(q[0, 0], q[0, 0], activation="tanh")
     with pytest.raises(ValueError):
         b.cache_evict(kp, kp, i, n, torch.zeros(1, 2, 64), i, 16)
