@@ -511,7 +511,7 @@ int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_
  * any more: attn_qk_norm_rope_append takes those separately.
  *
  *   block_table     : int32 [batch][max_blocks_per_seq], kv_lens: int32 [batch]
- *   sums            : fp32 [batch][n_kv_heads][max_blocks_per_seq * page_size]
+ *   sums            : fp32 [batch][n_kv_heads][max_blocks_per_seq * page_size], 16-byte aligned
  *   new_block_table : int32 [batch][new_max_blocks]; new_max_blocks * page_size >= budget. The
  *                     first ceil(min(n, budget) / page_size) entries of a row are used; those
  *                     pages must not occur in the old pages in use, nor twice (a page that does

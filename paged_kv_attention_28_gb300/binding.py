@@ -128,16 +128,29 @@ def _dt(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+# Small calls are bound by this file's host time, so the helpers hand ctypes plain integers and
+# decide the common case in one expression.
+
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The raw handle of a device's current stream, without building a torch.cuda.Stream (2 us).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
+    if (t.is_cuda and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -375,7 +388,7 @@ def flat_gemm(x, w, out=None, err_flag=None, stream=None):
 
 def _here(t: torch.Tensor, name: str):
     """The library launches on the current device: its tensors have to be there."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 

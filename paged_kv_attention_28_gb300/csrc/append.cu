@@ -10,16 +10,17 @@
 //
 // Angles: a position can be far (10^5 and more) and the angle matters modulo a full turn, so
 // an fp32 product loses what is needed (2^-24 of 10^5 rad is 0.006 rad). A pair's frequency is
-// kept as a 64-bit fixed-point fraction of a turn, F = frac(inv_freq / 2 pi) * 2^64 (one fp64
-// product per pair and CTA); position * F in wrapping 64-bit integers is then the exact phase
-// modulo one turn for any int32 position, off only by F's own rounding (2^-53 relative), and
-// sincospi of its leading bits gives cos and sin. No fp64 arithmetic per token.
+// taken as a 64-bit fixed-point fraction of a turn, F = frac(inv_freq / 2 pi) * 2^64, by an
+// integer product of the fp32 significand with 94 bits of 1 / 2 pi; position * F in wrapping
+// 64-bit integers is then the phase modulo one turn for any int32 position, off only by F's last
+// bit, and sincospi of its leading bits gives cos and sin. No fp64 arithmetic, whose rate here is
+// a 64th of fp32's.
 //
-// A CTA takes TOK tokens. Its threads first compute the tokens' cos and sin into shared memory,
-// one (token, pair) each, so that the rows of all heads share them; then groups of D / 8 lanes
-// take the rows (every query, key and value head of every token), 8 elements a lane in two
-// runs of 4 chosen so that both elements of a pair are in one lane: no exchange but the norm's
-// sum. kRows rows per group are loaded before any is used, to keep enough bytes in flight.
+// A CTA takes one token. Every thread asks for the rows of its first batch as soon as the token's
+// lengths are in; while they travel, one thread per pair computes the token's cos and sin
+// into shared memory, which the rows of all heads share. Groups of D / 8 lanes take the rows
+// (every query, key and value head), 8 elements a lane in two runs of 4 chosen so that both
+// elements of a pair are in one lane: no exchange but the norm's sum.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -59,82 +60,39 @@ struct Quad<__nv_bfloat16> {
   }
 };
 
-// What a token of the CTA does.
-struct Token {
-  int64_t in;    // index in [batch][chunk_len], or -1: nothing (padding)
-  int64_t page;  // (page * n_kv_heads) * page_size + slot of its K and V rows, or -1: bad
-};
+// frac(f / 2 pi) * 2^64, f finite.
+__device__ __forceinline__ uint64_t turn_fraction(float f) {
+  // 2^96 / 2 pi, rounded down: 94 bits
+  constexpr unsigned __int128 kTurns = ((unsigned __int128)0x28be60dbu << 64) | 0x9391054a7f09d5f4ull;
+  const uint32_t u = __float_as_uint(f);
+  const int field = (u >> 23) & 0xff;
+  const uint32_t m = (u & 0x7fffffu) | (field ? 0x800000u : 0u);
+  const int shift = 182 - (field ? field : 1);  // f = m 2^(field - 150), and 96 - 64 bits
+  const unsigned __int128 p = kTurns * m;
+  const uint64_t v = shift >= 128 ? 0 : shift >= 0 ? (uint64_t)(p >> shift) : shift > -64 ? (uint64_t)p << -shift : 0;
+  return (u >> 31) ? 0 - v : v;
+}
 
-template <typename T, int D, int TOK>
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   using Q4 = Quad<T>;
   using Raw = typename Q4::Raw;
   constexpr int L = D / 8;              // lanes per row
   constexpr int GROUPS = kThreads / L;  // rows a CTA works on at a time
-  __shared__ uint64_t s_freq[D / 2];
-  __shared__ int s_axis[D / 2];
-  __shared__ float2 s_cs[TOK][D / 2];
-  __shared__ Token s_tok[TOK];
-  __shared__ int s_live;
+  __shared__ __align__(16) float s_cos[D / 2];
+  __shared__ __align__(16) float s_sin[D / 2];
   const int tid = threadIdx.x;
   const int pairs = a.rotary_dim / 2;
-  const int64_t n_tokens = (int64_t)a.batch * a.chunk_len;
-  const int64_t t0 = (int64_t)blockIdx.x * TOK;
-
-  if (tid == 0) s_live = 0;
-  __syncthreads();
-  if (tid < TOK && t0 + tid < n_tokens) {
-    const int64_t t = t0 + tid;
-    const int b = (int)(t / a.chunk_len), i = (int)(t % a.chunk_len);
-    const int64_t len = __ldg(a.prefix_lens + b);
-    const int64_t n = a.chunk_lens ? __ldg(a.chunk_lens + b) : a.chunk_len;
-    Token k{-1, -1};
-    if (len < 0 || n < 0 || n > a.chunk_len || len + n > (int64_t)a.max_blocks * a.page_size) {
-      set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
-      if (n < 0 || n > a.chunk_len || i < n) k.in = t;
-    } else if (i < n) {
-      const int64_t at = len + i;
-      const int page = __ldg(a.block_table + (int64_t)b * a.max_blocks + at / a.page_size);
-      k.in = t;
-      if (page < 0 || page >= a.num_pages)
-        set_err(a.err_flag, PKV_DEVERR_BAD_PAGE);
-      else
-        k.page = (int64_t)page * a.n_kv_heads * a.page_size + at % a.page_size;
-    }
-    s_tok[tid] = k;
-    if (k.in >= 0) s_live = 1;
-  } else if (tid < TOK) {
-    s_tok[tid] = Token{-1, -1};
-  }
-  if (tid >= kThreads - pairs) {  // (pairs <= 64: not the threads that look the tokens up)
-    const int p = tid - (kThreads - pairs);
-    const float f = __ldg(a.inv_freq + p);
-    const double turns = (double)f * 0.15915494309189535;  // 1 / (2 pi)
-    s_freq[p] = (uint64_t)((turns - floor(turns)) * 18446744073709551616.0);
-    int axis = a.pair_axis ? __ldg(a.pair_axis + p) : 0;
-    if (axis < 0 || axis >= a.n_axes) {
-      set_err(a.err_flag, PKV_DEVERR_BAD_AXIS);
-      axis = -1;
-    }
-    s_axis[p] = fabsf(f) < INFINITY ? axis : -1;  // -1: the pair's outputs are NaN
-  }
-  __syncthreads();
-  if (!s_live) return;
-  for (int x = tid; x < TOK * pairs; x += kThreads) {
-    const int k = x / pairs, p = x % pairs;
-    const int64_t t = s_tok[k].in;
-    if (t < 0) continue;
-    const int axis = s_axis[p];
-    float2 cs = make_float2(NAN, NAN);
-    if (axis >= 0) {
-      const int64_t pos = a.positions ? __ldg(a.positions + axis * n_tokens + t)
-                                      : (int64_t)__ldg(a.prefix_lens + t / a.chunk_len) + t % a.chunk_len;
-      const int64_t phase = (int64_t)((uint64_t)pos * s_freq[p]);  // 2^64 to a turn
-      sincospif((float)phase * 1.0842021724855044e-19f, &cs.y, &cs.x);  // 2^-63: half turns
-    }
-    s_cs[k][p] = cs;
-  }
-  __syncthreads();
+  const int64_t t = blockIdx.x;
+  const int b = (int)(t / a.chunk_len), i = (int)(t % a.chunk_len);
+  const int64_t len = __ldg(a.prefix_lens + b);
+  const int64_t n = a.chunk_lens ? __ldg(a.chunk_lens + b) : a.chunk_len;
+  const bool bad_n = n < 0 || n > a.chunk_len;
+  if (!bad_n && i >= n) return;  // padding
+  const int64_t at = len + i;
+  const bool bad_len = bad_n || len < 0 || len + n > (int64_t)a.max_blocks * a.page_size;
+  int page = -1;
+  if (!bad_len) page = __ldg(a.block_table + (int64_t)b * a.max_blocks + at / a.page_size);
 
   const int l = tid % L, group = tid / L;
   const int rows = a.n_qo_heads + 2 * a.n_kv_heads;
@@ -142,30 +100,52 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   const bool turned = 8 * l < a.rotary_dim;
   const int o0 = !turned || a.interleaved ? 8 * l : 4 * l;
   const int o1 = !turned || a.interleaved ? 8 * l + 4 : pairs + 4 * l;
-  for (int base = 0; base < TOK * rows; base += GROUPS * kRows) {
-    Raw lo[kRows], hi[kRows];
-    int kind[kRows];  // 0 q, 1 k, 2 v, -1 nothing
+  Raw lo[kRows], hi[kRows];
+  auto load = [&](int base) {
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int x = base + u * GROUPS + group;
-      const int k = x / rows, r = x % rows;
-      kind[u] = -1;
+      const int r = base + u * GROUPS + group;
       lo[u] = Raw{}, hi[u] = Raw{};
-      if (x < TOK * rows && s_tok[k].in >= 0) {
-        const int64_t t = s_tok[k].in;
-        kind[u] = r < a.n_qo_heads ? 0 : r < a.n_qo_heads + a.n_kv_heads ? 1 : 2;
-        const int h = r - (kind[u] == 0 ? 0 : kind[u] == 1 ? a.n_qo_heads : a.n_qo_heads + a.n_kv_heads);
-        const T* src = static_cast<const T*>(kind[u] == 0 ? a.q : kind[u] == 1 ? a.k : a.v) +
-                       t * (kind[u] == 0 ? a.q_stride : kind[u] == 1 ? a.k_stride : a.v_stride) + (int64_t)h * D;
+      if (r < rows) {
+        const bool is_q = r < a.n_qo_heads, is_k = r < a.n_qo_heads + a.n_kv_heads;
+        const int h = r - (is_q ? 0 : is_k ? a.n_qo_heads : a.n_qo_heads + a.n_kv_heads);
+        const T* src = static_cast<const T*>(is_q ? a.q : is_k ? a.k : a.v) +
+                       t * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) + (int64_t)h * D;
         lo[u] = *reinterpret_cast<const Raw*>(src + o0);
         hi[u] = *reinterpret_cast<const Raw*>(src + o1);
       }
     }
+  };
+  load(0);
+
+  if (tid < pairs) {
+    const float f = __ldg(a.inv_freq + tid);
+    int axis = a.pair_axis ? __ldg(a.pair_axis + tid) : 0;
+    if (axis < 0 || axis >= a.n_axes) {
+      set_err(a.err_flag, PKV_DEVERR_BAD_AXIS);
+      axis = -1;
+    }
+    float c = NAN, s = NAN;
+    if (axis >= 0 && fabsf(f) < INFINITY) {
+      const int64_t pos = a.positions ? __ldg(a.positions + axis * ((int64_t)a.batch * a.chunk_len) + t) : at;
+      const int64_t phase = (int64_t)((uint64_t)pos * turn_fraction(f));  // 2^64 to a turn
+      sincospif((float)phase * 1.0842021724855044e-19f, &s, &c);          // 2^-63: half turns
+    }
+    s_cos[tid] = c;
+    s_sin[tid] = s;
+  }
+  if (page < 0 || page >= a.num_pages) {
+    page = -1;
+    if (tid == 0) set_err(a.err_flag, bad_len ? PKV_DEVERR_BAD_LEN : PKV_DEVERR_BAD_PAGE);
+  }
+  const int64_t slot = ((int64_t)page * a.n_kv_heads) * a.page_size + at % a.page_size;  // of KV head 0
+  __syncthreads();
+
+  for (int base = 0;;) {
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int x = base + u * GROUPS + group;
-      const int k = min(x / rows, TOK - 1), r = x % rows;
-      const T* w = static_cast<const T*>(kind[u] == 0 ? a.q_norm : a.k_norm);
+      const int r = base + u * GROUPS + group;
+      const bool is_q = r < a.n_qo_heads, is_k = r < a.n_qo_heads + a.n_kv_heads;
       float v[8];
       Q4::get(lo[u], v, 0);
       Q4::get(hi[u], v, 4);
@@ -174,9 +154,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
       for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
 #pragma unroll
       for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      if (kind[u] < 0) continue;
-      const Token tok = s_tok[k];
-      if (kind[u] < 2) {
+      if (r >= rows) continue;
+      if (is_k) {  // (queries too)
+        const T* w = static_cast<const T*>(is_q ? a.q_norm : a.k_norm);
         if (w) {
           const float s = rsqrtf(ss * (1.0f / D) + a.eps);
           float wv[8];
@@ -186,18 +166,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
           for (int e = 0; e < 8; ++e) v[e] = v[e] * s * wv[e];
         }
         if (turned) {
+          const float4 c4 = *reinterpret_cast<const float4*>(s_cos + 4 * l);
+          const float4 s4 = *reinterpret_cast<const float4*>(s_sin + 4 * l);
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+          if (a.interleaved) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 cs = s_cs[k][4 * l + j];
-            const float xa = a.interleaved ? v[2 * j] : v[j], xb = a.interleaved ? v[2 * j + 1] : v[j + 4];
-            const float za = xa * cs.x - xb * cs.y, zb = xb * cs.x + xa * cs.y;
-            if (a.interleaved)
-              v[2 * j] = za, v[2 * j + 1] = zb;
-            else
-              v[j] = za, v[j + 4] = zb;
+            for (int j = 0; j < 4; ++j) {
+              const float xa = v[2 * j], xb = v[2 * j + 1];
+              v[2 * j] = xa * c[j] - xb * s[j];
+              v[2 * j + 1] = xb * c[j] + xa * s[j];
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float xa = v[j], xb = v[j + 4];
+              v[j] = xa * c[j] - xb * s[j];
+              v[j + 4] = xb * c[j] + xa * s[j];
+            }
           }
         }
-        if (kind[u] == 0 && tok.page < 0) {
+        if (is_q && page < 0) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = NAN;
         }
@@ -205,28 +193,25 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
         hi[u] = Q4::put(v, 4);
       }
       T* dst;
-      if (kind[u] == 0) {
-        dst = static_cast<T*>(a.q_out) + (tok.in * a.n_qo_heads + r) * D;
+      if (is_q) {
+        dst = static_cast<T*>(a.q_out) + (t * a.n_qo_heads + r) * D;
       } else {
-        if (tok.page < 0) continue;
-        const int h = r - a.n_qo_heads - (kind[u] == 2 ? a.n_kv_heads : 0);
-        dst = static_cast<T*>(kind[u] == 1 ? a.k_pages : a.v_pages) + (tok.page + (int64_t)h * a.page_size) * D;
+        if (page < 0) continue;
+        const int h = r - a.n_qo_heads - (is_k ? 0 : a.n_kv_heads);
+        dst = static_cast<T*>(is_k ? a.k_pages : a.v_pages) + (slot + (int64_t)h * a.page_size) * D;
       }
       *reinterpret_cast<Raw*>(dst + o0) = lo[u];
       *reinterpret_cast<Raw*>(dst + o1) = hi[u];
     }
+    base += GROUPS * kRows;
+    if (base >= rows) break;
+    load(base);
   }
 }
 
 template <typename T, int D>
 int launch_t(const AppendArgs& a, cudaStream_t stream) {
-  const int64_t n = (int64_t)a.batch * a.chunk_len;
-  // Few tokens: one per CTA, so that they spread over the SMs. Many: four, so that a thread
-  // computes about one angle and the rows dominate.
-  if (n <= 1024)
-    append_kernel<T, D, 1><<<(unsigned)n, kThreads, 0, stream>>>(a);
-  else
-    append_kernel<T, D, 4><<<(unsigned)((n + 3) / 4), kThreads, 0, stream>>>(a);
+  append_kernel<T, D><<<(unsigned)((int64_t)a.batch * a.chunk_len), kThreads, 0, stream>>>(a);
   return check_launch(cudaGetLastError());
 }
 

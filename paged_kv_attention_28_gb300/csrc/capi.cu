@@ -536,7 +536,7 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
   if (batch == 0) return PKV_OK;
   if (!k_pages || !v_pages || !block_table || !kv_lens || !sums || !new_block_table || !kept || !new_lens || !new_sums)
     return PKV_ERR_INVALID_ARG;
-  if (!aligned16(k_pages) || !aligned16(v_pages)) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(sums)) return PKV_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || page_size != 16) return PKV_ERR_UNSUPPORTED;
   if (batch > 65535 || n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
   EvictArgs a{k_pages, v_pages, block_table, kv_lens, sums, new_block_table, kept, new_lens, new_sums, batch,

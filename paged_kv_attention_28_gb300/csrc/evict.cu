@@ -5,12 +5,19 @@
 // order. The kept rows of K and V are gathered into the pages of a new table, so shared source
 // pages stay whole and no row is overwritten before it is read.
 //
-// Two kernels. The selection is one CTA per (sequence, KV head): a float's order-preserving
-// bits are searched for the m-th largest by three passes of 11, 11 and 10 bits, each a
-// histogram in shared memory of the values that share the digits found so far; only the first
-// pass has every value in it. Then each warp, which holds a contiguous run of tokens, counts
-// what it keeps, one scan over the warps places the runs, and the kept indices and sums are
-// written in order. The gather is one lane group per kept row, K and V of four rows in flight.
+// Two kernels. The selection is one CTA per (sequence, KV head). A token becomes a 32-bit key,
+// once, in shared memory: the sums' order-preserving bits, above them NaN, above all the sinks
+// and recents, so that what is kept is the `budget` largest keys. The last of them is searched
+// for by passes of 8 bits, each a histogram of the keys that share the digits found so far,
+// until a pass needs a whole bin. Sums cluster (many are equal, most share an exponent) and
+// atomics on one address take turns, so a bin has 8 counters, by lane. Then each warp, which holds a
+// contiguous run of tokens, counts what it keeps, one scan over the warps places the runs, and
+// the kept indices and sums are written in order. Rows past kSmemTokens are read again in
+// each pass.
+//
+// What bounds the selection: the atomics of long rows (5 clocks a warp), for short ones the
+// instructions that every warp runs for a few tokens each, so those get 256 threads. The gather is one lane group per kept row, K and V
+// of four rows in flight, and runs at the copy bandwidth.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -21,34 +28,59 @@
 namespace pkv {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kDigits = 256;
+constexpr int kCopies = 8;                // counters of a bin
+constexpr int kGroup = 4;                 // consecutive tokens of a lane
+constexpr int kShortTokens = 4096;        // rows up to this length: 256 threads
+constexpr int kSmemTokens = 13 * 4096;    // 208 KiB, beside the 8 KiB of counters
 
-// Bits that order as the floats do; both zeros are equal, and NaN is above every number.
+constexpr uint32_t kAlways = 0xffffffffu;  // sinks and recents
+
+// Bits that order as the floats do, all above 0; both zeros are equal, NaN is above every number.
 __device__ __forceinline__ uint32_t order_bits(float x) {
-  if (x != x) return 0xffffffffu;
+  if (x != x) return kAlways - 1;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Tokens per thread held in registers, E; 0: read again from memory in each pass.
-template <int E>
+// The float of order_bits (a zero comes back positive, a NaN as the canonical one).
+__device__ __forceinline__ float from_order_bits(uint32_t k) {
+  return __uint_as_float(k == kAlways - 1 ? 0x7fffffffu : (k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// Counts in shared memory where `on`, without a branch around the atomic.
+__device__ __forceinline__ void count_if(bool on, uint32_t addr) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(addr), "r"((uint32_t)on)
+      : "memory");
+}
+
+template <bool SMEM, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) {
-  __shared__ int s_hist[kBins];
+  constexpr int kSelWarps = kSelThreads / 32, kWave = kGroup * kSelThreads;
+  constexpr int kPerBin = kSelThreads / kDigits;  // threads that add up a bin's counters
+  __shared__ __align__(16) int s_hist[kDigits * kCopies];
   __shared__ int s_warp[kSelWarps], s_warp2[kSelWarps];
-  __shared__ int s_digit, s_above;
+  __shared__ int s_digit, s_above, s_count;
+  extern __shared__ __align__(16) uint32_t s_row[];
   const int b = blockIdx.y, h = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int cap = a.max_blocks * a.page_size, new_cap = a.new_max_blocks * a.page_size;
+  const int64_t row = (int64_t)b * a.n_kv_heads + h;
+  const float* sums = a.sums + row * cap;
   int n = __ldg(a.kv_lens + b);
+  // The first wave of sums is asked for beside the length (it lies inside the row: rows are
+  // 16-byte aligned multiples of 16 tokens).
+  auto fetch = [&](int t) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s_row + t)), "l"(sums + t) : "memory");
+  };
+  if (SMEM && kGroup * tid < cap) fetch(kGroup * tid);
+  for (int i = tid; i < kDigits * kCopies; i += kSelThreads) s_hist[i] = 0;
   if (n < 0 || n > cap) {
     if (tid == 0) set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
     n = 0;
   }
-  const int64_t row = (int64_t)b * a.n_kv_heads + h;
-  const float* sums = a.sums + row * cap;
   float* new_sums = a.new_sums + row * new_cap;
   int* kept = a.kept + row * a.budget;
   const int n_new = min(n, a.budget);
@@ -58,111 +90,160 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
   if (n <= a.budget) {
     for (int j = tid; j < n; j += kSelThreads) {
       kept[j] = j;
-      new_sums[j] = sums[j];
+      new_sums[j] = __ldg(sums + j);
     }
+    if (SMEM) asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
-  // The candidates [lo, hi) and how many of them stay: 0 <= m < hi - lo.
-  const int lo = a.n_sink, hi = n - a.n_recent, m = a.budget - a.n_sink - a.n_recent;
-  const int per = (n + kSelThreads - 1) / kSelThreads;  // tokens per lane; a warp's are contiguous
-  const int first = warp * 32 * per + lane;
-  float held[E > 0 ? E : 1];
-  if constexpr (E > 0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int t = first + 32 * e;
-      held[e] = e < per && t < n ? __ldg(sums + t) : 0.0f;
-    }
+  const int lo = a.n_sink, hi = n - a.n_recent;  // [lo, hi): the tokens that are ranked by their sums
+  auto key_of = [&](int t, float x) { return t >= n ? 0u : t < lo || t >= hi ? kAlways : order_bits(x); };
+  auto keys_of = [&](int t, const float4& x) {
+    return make_uint4(key_of(t, x.x), key_of(t + 1, x.y), key_of(t + 2, x.z), key_of(t + 3, x.w));
+  };
+  const int waves = (n + kWave - 1) / kWave;
+  if constexpr (SMEM) {
+    for (int t = kWave + kGroup * tid; t < n; t += kWave) fetch(t);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
-  auto value = [&](int e, int t) { return E > 0 ? held[E > 0 ? e : 0] : __ldg(sums + t); };
+  // A warp's tokens are contiguous: group e of lane l is tokens first + 128 e .. + 3.
+  const int first = warp * (32 * kGroup) * waves + kGroup * lane;
+  auto sums_at = [&](int t) {
+    if (t >= n) return make_float4(0.f, 0.f, 0.f, 0.f);
+    return SMEM ? *reinterpret_cast<const float4*>(s_row + t) : __ldg(reinterpret_cast<const float4*>(sums + t));
+  };
+  auto keys = [&](int e, bool raw) {
+    const int t = first + 32 * kGroup * e;
+    if (SMEM && !raw) return *reinterpret_cast<const uint4*>(s_row + t);
+    const uint4 k = keys_of(t, sums_at(t));
+    if (SMEM) *reinterpret_cast<uint4*>(s_row + t) = k;  // the first pass turns the sums into keys
+    return k;
+  };
 
-  // found: the digits of the m-th largest key found so far; need: how many of the keys that
-  // share them are kept. Keys above are all kept.
+  // found: the digits of the budget-th largest key found so far (those in mask); need: how many
+  // of the keys that share them are kept. Keys above are all kept.
   uint32_t found = 0, mask = 0;
-  int need = m;
-  if (m > 0) {
+  int need = a.budget;
+  const uint32_t column = smem_u32(s_hist) + 4 * (lane & (kCopies - 1));
+  __syncthreads();
+#pragma unroll 1
+  for (int shift = 24; shift >= 0; shift -= 8) {
+#pragma unroll 2
+    for (int e = 0; e < waves; ++e) {
+      const uint4 k4 = keys(e, shift == 24);
+      const uint32_t k[kGroup] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
-      for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-      __syncthreads();
+      for (int i = 0; i < kGroup; ++i)
+        count_if((k[i] & mask) == found, column + ((k[i] >> shift) & 255u) * (4 * kCopies));
+    }
+    __syncthreads();
+    // kPerBin threads add up a bin's counters (and clear them for the next pass); `above`: the
+    // keys in higher bins, first within the warp, then those of the warps above it
+    const int bin = tid / kPerBin;
+    int c = 0;
+    {
+      int2* p = reinterpret_cast<int2*>(s_hist) + tid * (kCopies / kPerBin / 2);
 #pragma unroll
-      for (int e = 0; e < (E > 0 ? E : per); ++e) {
-        const int t = first + 32 * e;
-        if (e < per && t >= lo && t < hi) {
-          const uint32_t key = order_bits(value(e, t));
-          if ((key & mask) == found) atomicAdd(&s_hist[(key >> shift) & digit_mask], 1);
-        }
+      for (int i = 0; i < kCopies / kPerBin / 2; ++i) {
+        const int2 x = p[i];
+        p[i] = make_int2(0, 0);
+        c += x.x + x.y;
       }
-      __syncthreads();
-      // bins from the top: thread i has bins 2047 - 2 i and 2046 - 2 i
-      const int c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid];
-      int incl = c0 + c1;
+    }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) s_warp[warp] = incl;
-      __syncthreads();
-      int before = 0;
-      for (int w = 0; w < kSelWarps; ++w) before += w < warp ? s_warp[w] : 0;
-      const int above = before + incl - c0 - c1;  // keys in the bins above this thread's
-      if (above < need && above + c0 >= need) {
-        s_digit = kBins - 1 - 2 * tid;
-        s_above = above;
-      } else if (above + c0 < need && above + c0 + c1 >= need) {
-        s_digit = kBins - 2 - 2 * tid;
-        s_above = above + c0;
-      }
-      __syncthreads();
-      found |= (uint32_t)s_digit << shift;
-      mask |= digit_mask << shift;
-      need -= s_above;
+    for (int o = 1; o < kPerBin; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    int above = c;
+#pragma unroll
+    for (int o = kPerBin; o < 32; o <<= 1) {
+      const int y = __shfl_down_sync(0xffffffffu, above, o);
+      if (lane + o < 32) above += y;
+    }
+    if (lane == 0) s_warp[warp] = above;
+    above -= c;
+    __syncthreads();
+    above += __reduce_add_sync(0xffffffffu, lane > warp && lane < kSelWarps ? s_warp[lane] : 0);
+    if (above < need && above + c >= need) {  // one bin in all
+      s_digit = bin;
+      s_above = above;
+      s_count = c;
+    }
+    __syncthreads();
+    found |= (uint32_t)s_digit << shift;
+    mask |= 255u << shift;
+    need -= s_above;
+    if (s_count == need) break;  // the whole bin is kept: its keys need no more digits
+  }
+  // Kept: keys whose found digits are above, and the first `need` that share them.
+  int sure = 0, equal = 0;
+#pragma unroll 2
+  for (int e = 0; e < waves; ++e) {
+    const uint4 k4 = keys(e, false);
+    const uint32_t k[kGroup] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      sure += (k[i] & mask) > found;
+      equal += (k[i] & mask) == found;
     }
   }
-  // Kept: sinks, recents, keys above `found`, and the first `need` that equal it (m = 0: the
-  // sinks and recents alone).
-  int sure = 0, equal = 0;
-#pragma unroll
-  for (int e = 0; e < (E > 0 ? E : per); ++e) {
-    const int t = first + 32 * e;
-    const bool in = e < per && t < n;
-    const bool cand = in && t >= lo && t < hi;
-    const uint32_t key = cand ? order_bits(value(e, t)) : 0u;
-    sure += __popc(__ballot_sync(0xffffffffu, in && (!cand || (m > 0 && key > found))));
-    equal += __popc(__ballot_sync(0xffffffffu, cand && m > 0 && key == found));
-  }
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  equal = __reduce_add_sync(0xffffffffu, equal);
   if (lane == 0) {
     s_warp[warp] = sure;
     s_warp2[warp] = equal;
   }
   __syncthreads();
-  int sure_before = 0, eq_before = 0;
-  for (int w = 0; w < kSelWarps; ++w) {
-    sure_before += w < warp ? s_warp[w] : 0;
-    eq_before += w < warp ? s_warp2[w] : 0;
-  }
+  int at = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0);
+  int eq_left = need - __reduce_add_sync(0xffffffffu, lane < warp ? s_warp2[lane] : 0);  // kept of this warp's equal keys
+  at += need - max(eq_left, 0);  // where the warp's first kept token goes
+  // Only the warp in which the equal keys run out has to count them; before it all are kept.
+  const bool count_equal = eq_left > 0 && eq_left < equal;
+  // nothing is above kAlways, and this warp has no equal key left to keep
+  const int groups = eq_left <= 0 && found == kAlways ? 0 : waves;
+  const uint32_t least = eq_left > 0 ? found : found + 1;
   const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 1
+  for (int e = 0; e < groups; ++e) {
+    const int t = first + 32 * kGroup * e;
+    const uint4 k4 = keys(e, false);
+    const uint32_t full[kGroup] = {k4.x, k4.y, k4.z, k4.w};
+    const uint32_t k[kGroup] = {k4.x & mask, k4.y & mask, k4.z & mask, k4.w & mask};
+    bool keep[kGroup];
 #pragma unroll
-  for (int e = 0; e < (E > 0 ? E : per); ++e) {
-    const int t = first + 32 * e;
-    const bool in = e < per && t < n;
-    const bool cand = in && t >= lo && t < hi;
-    const float x = in ? value(e, t) : 0.0f;
-    const uint32_t key = cand ? order_bits(x) : 0u;
-    const bool is_sure = in && (!cand || (m > 0 && key > found));
-    const bool is_eq = cand && m > 0 && key == found;
-    const unsigned ms = __ballot_sync(0xffffffffu, is_sure), me = __ballot_sync(0xffffffffu, is_eq);
-    const int eq_rank = eq_before + __popc(me & below);
-    const int j = sure_before + __popc(ms & below) + min(eq_rank, need);
-    if (is_sure || (is_eq && eq_rank < need)) {
-      kept[j] = t;
-      new_sums[j] = x;
+    for (int i = 0; i < kGroup; ++i) keep[i] = k[i] >= least;
+    if (count_equal) {
+      unsigned m[kGroup];
+      int rank = 0, all = 0;
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        m[i] = __ballot_sync(0xffffffffu, k[i] == found);
+        rank += __popc(m[i] & below);
+        all += __popc(m[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        keep[i] = k[i] > found || (k[i] == found && rank < eq_left);
+        rank += k[i] == found;
+      }
+      eq_left -= all;
     }
-    sure_before += __popc(ms);
-    eq_before += __popc(me);
+    int j = at;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      const unsigned m = __ballot_sync(0xffffffffu, keep[i]);
+      j += __popc(m & below);
+      at += __popc(m);
+    }
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      if (keep[i]) kept[j] = t + i;
+      if (keep[i] && full[i] != kAlways) new_sums[j] = from_order_bits(full[i]);
+      j += keep[i];
+    }
+  }
+  // sinks and recents keep their order around the others, so their places are known
+  for (int j = tid; j < a.n_sink + a.n_recent; j += kSelThreads) {
+    const int back = j < a.n_sink ? 0 : j - a.n_sink - a.n_recent;  // < 0: from the end
+    const int to = back < 0 ? a.budget + back : j;
+    new_sums[to] = __ldg(sums + (back < 0 ? n + back : j));
   }
 }
 
@@ -238,12 +319,16 @@ int launch_gather(const EvictArgs& a, cudaStream_t stream) {
 int launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const int64_t cap = (int64_t)a.max_blocks * a.page_size;
   const dim3 grid((unsigned)a.n_kv_heads, (unsigned)a.batch);
-  if (cap <= 8 * kSelThreads)
-    select_kernel<8><<<grid, kSelThreads, 0, stream>>>(a);
-  else if (cap <= 32 * kSelThreads)
-    select_kernel<32><<<grid, kSelThreads, 0, stream>>>(a);
-  else
-    select_kernel<0><<<grid, kSelThreads, 0, stream>>>(a);
+  if (cap <= kShortTokens) {
+    select_kernel<true, 256><<<grid, 256, (size_t)((cap + 1023) / 1024) * 4096, stream>>>(a);
+  } else if (cap <= kSmemTokens) {
+    static FuncConfigured configured;
+    if (!configured.ensure(reinterpret_cast<const void*>(select_kernel<true, 1024>), kSmemTokens * 4))
+      return PKV_ERR_LAUNCH;
+    select_kernel<true, 1024><<<grid, 1024, (size_t)((cap + 4095) / 4096) * 16384, stream>>>(a);
+  } else {
+    select_kernel<false, 1024><<<grid, 1024, 0, stream>>>(a);
+  }
   const int rc = check_launch(cudaGetLastError());
   if (rc != PKV_OK) return rc;
   switch (a.head_dim * (a.dtype == PKV_F32 ? 4 : 2)) {

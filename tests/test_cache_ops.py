@@ -134,7 +134,7 @@ def evict_args(b, **kw):
 
 
 @pytest.mark.parametrize("bad,want", [
-    (dict(kp=None), -1), (dict(kept=None), -1), (dict(ns=None), -1), (dict(nt=None), -1), (dict(kp=ODD), -1),
+    (dict(kp=None), -1), (dict(kept=None), -1), (dict(ns=None), -1), (dict(nt=None), -1), (dict(kp=ODD), -1), (dict(s=ODD), -1),
     (dict(budget=0), -1), (dict(budget=33), -1), (dict(sink=-1), -1), (dict(recent=-1), -1), (dict(sink=25), -1),
     (dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), -1), (dict(batch=-1), -1), (dict(mb=0), -1), (dict(nb=0), -1),
     (dict(dt=5), -1), (dict(mb=1 << 28), -1), (dict(d=96), -2), (dict(page=32, budget=64), -2), (dict(batch=70000), -2),

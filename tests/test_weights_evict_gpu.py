@@ -191,6 +191,11 @@ def test_evict_orders_ties_and_odd_values(b, kind, lens, budget):
     check_evict(b, lens, 2, 64, "bf16", budget, 3, 11, kind=kind)
 
 
+@pytest.mark.parametrize("sink,recent,budget", [(16, 32, 48), (0, 48, 48), (48, 0, 48), (16, 31, 48), (0, 0, 48)])
+def test_evict_when_sinks_and_recents_fill_the_budget(b, sink, recent, budget):
+    check_evict(b, [700, 49, 5000], 2, 64, "bf16", budget, sink, recent, kind="odd")
+
+
 def test_evict_reads_no_further_than_the_length(b):
     # a table wider than the sequences: entries and sums past the length are poison
     table, new, kp, vp, s, ln = make_evict(6, [40, 70], 2, 64, "bf16", 32, blocks=40)
