@@ -1,6 +1,7 @@
 """ctypes binding to ``libpkvattn.so``: the C ABI declared in ``include/pkv_attn.h``.
 
-This layer only marshals arguments. It turns torch CUDA tensors into device
+This layer only marshals arguments, through ctypes or, for the operators whose smallest calls
+take less time than that, through the CPython module ``_pycall``. It turns torch CUDA tensors into device
 pointers, checks shapes and dtypes on the host, and passes the current CUDA
 stream. Every step of the computation runs in the library's kernels. If the
 library is missing, importing this module raises; nothing falls back to
@@ -109,6 +110,9 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+# The checks and calls of the operators whose small calls are bound by the host (csrc/pycall.c).
+from . import _pycall  # noqa: E402  (needs the library)
 
 
 def status_string(status: int) -> str:
@@ -386,26 +390,22 @@ def flat_gemm(x, w, out=None, err_flag=None, stream=None):
 
 # --------------------------------------------------------------------------- cache write
 
-def _here(t: torch.Tensor, name: str):
-    """The library launches on the current device: its tensors have to be there."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+_fast_need = _pycall.need
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
+def _token_rows(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
     """Checks ``[B, C, H, D]`` whose head rows are contiguous per token; the token stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     B, C, H, D = shape
     sb, sc, sh, sd = t.stride()
-    token = sc if C > 1 else sb if B > 1 else H * D
-    if (sd != 1 and D > 1) or (sh != D and H > 1) or (B > 1 and C > 1 and sb != C * sc):
-        raise ValueError(f"{name} must hold each token's heads contiguously at one stride per token, got {t.stride()}")
-    return token
+    if (sd == 1 or D == 1) and (sh == D or H == 1) and (sb == C * sc or B == 1 or C == 1):
+        return sc if C > 1 else sb if B > 1 else H * D
+    raise ValueError(f"{name} must hold each token's heads contiguously at one stride per token, got {t.stride()}")
 
 
 def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chunk_lens=None, positions=None,
@@ -416,41 +416,40 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chu
     ``q`` ``[B, C, Hq, D]`` and ``k``, ``v`` ``[B, C, Hkv, D]`` may be slices of one fused
     projection; ``positions`` ``[n_axes, B, C]`` (or ``[B, C]`` for one axis). Returns the
     rotated queries ``[B, C, Hq, D]``."""
-    B, C, Hq, D = q.shape
+    B, C, Hq, D = rows = q.shape
     num_pages, Hkv, P, D2 = k_pages.shape
-    assert D2 == D
+    if D2 != D:
+        raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
     max_blocks = block_table.shape[1]
-    qs = _token_rows(q, "q", q.dtype, (B, C, Hq, D))
-    ks = _token_rows(k, "k", q.dtype, (B, C, Hkv, D))
-    vs = _token_rows(v, "v", q.dtype, (B, C, Hkv, D))
-    _here(q, "q")
-    _need(k_pages, "k_pages", q.dtype)
-    _need(v_pages, "v_pages", q.dtype, k_pages.shape)
-    _need(block_table, "block_table", torch.int32, (B, max_blocks))
-    _need(prefix_lens, "prefix_lens", torch.int32, (B,))
-    if chunk_lens is not None:
-        _need(chunk_lens, "chunk_lens", torch.int32, (B,))
+    dev, dtype, need = torch.cuda.current_device() if q.is_cuda else -2, q.dtype, _fast_need
+    qs = _token_rows(q, "q", dev, dtype, rows)
+    ks = _token_rows(k, "k", dev, dtype, (B, C, Hkv, D))
+    vs = _token_rows(v, "v", dev, dtype, (B, C, Hkv, D))
     n_axes = 1
     if positions is not None:
-        n_axes = positions.shape[0] if positions.dim() == 3 else 1
-        _need(positions, "positions", torch.int32, (n_axes, B, C) if positions.dim() == 3 else (B, C))
+        if positions.dim() == 3:
+            n_axes = positions.shape[0]
+            positions = need(positions, "positions", dev, torch.int32, (n_axes, B, C))
+        else:
+            positions = need(positions, "positions", dev, torch.int32, (B, C))
     rot = 0
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float32)
         rot = 2 * inv_freq.numel()
-    if pair_axis is not None:
-        _need(pair_axis, "pair_axis", torch.int32, (rot // 2,))
-    for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None:
-            _need(t, n, q.dtype, (D,))
+        inv_freq = need(inv_freq, "inv_freq", dev, torch.float32, (rot // 2,))
     if out is None:
-        out = torch.empty((B, C, Hq, D), dtype=q.dtype, device=q.device)
-    _need(out, "out", q.dtype, (B, C, Hq, D))
-    st = lib.attn_qk_norm_rope_append(_ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(q_norm), _ptr(k_norm), float(eps),
-                                      _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(positions), n_axes,
-                                      _ptr(pair_axis), _ptr(block_table), _ptr(prefix_lens), _ptr(chunk_lens),
-                                      _ptr(out), _ptr(k_pages), _ptr(v_pages), B, C, max_blocks, num_pages, Hq, Hkv,
-                                      D, P, _dt(q), _ptr(err_flag), _stream(stream))
+        out = torch.empty((B, C, Hq, D), dtype=dtype, device=q.device)
+    st = _pycall.attn_qk_norm_rope_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+        None if q_norm is None else need(q_norm, "q_norm", dev, dtype, (D,)),
+        None if k_norm is None else need(k_norm, "k_norm", dev, dtype, (D,)), eps, inv_freq, rot,
+        1 if interleaved else 0, positions, n_axes,
+        None if pair_axis is None else need(pair_axis, "pair_axis", dev, torch.int32, (rot // 2,)),
+        need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
+        need(prefix_lens, "prefix_lens", dev, torch.int32, (B,)),
+        None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, torch.int32, (B,)),
+        need(out, "out", dev, dtype, rows), need(k_pages, "k_pages", dev, dtype, None),
+        need(v_pages, "v_pages", dev, dtype, k_pages.shape), B, C, max_blocks, num_pages, Hq, Hkv, D, P, _dt(q),
+        _ptr(err_flag), _stream(stream))
     _check(st, "attn_qk_norm_rope_append")
     return out
 
@@ -473,18 +472,17 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums,
     ``attn_decode_paged_weights``. Returns ``(out, lse, sums)``."""
     B, Hq, D = q.shape
     num_pages, Hkv, P, D2 = k_pages.shape
-    assert D2 == D
+    if D2 != D:
+        raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
     max_blocks = block_table.shape[1]
-    _need(q, "q")
-    _here(q, "q")
-    _need(k_pages, "k_pages", q.dtype)
-    _need(v_pages, "v_pages", q.dtype, k_pages.shape)
-    _need(block_table, "block_table", torch.int32, (B, max_blocks))
-    _need(kv_lens, "kv_lens", torch.int32, (B,))
-    _need(weight_sums, "weight_sums", torch.float32, (B, Hkv, max_blocks * P))
+    dev, dtype, need = torch.cuda.current_device() if q.is_cuda else -2, q.dtype, _fast_need
+    q_ptr = need(q, "q", dev, None, None)
+    sums = (B, Hkv, max_blocks * P)
+    in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, torch.float32, sums)
     if sums_out is None:
         sums_out = weight_sums
-    _need(sums_out, "sums_out", torch.float32, weight_sums.shape)
+    else:
+        out_ptr = need(sums_out, "sums_out", dev, torch.float32, sums)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -492,11 +490,14 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums,
     if workspace is None:
         workspace = alloc_workspace(decode_weights_workspace_size(B, max_blocks, Hq, Hkv, D, P, num_splits, _dt(q)),
                                     q.device)
-    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib.attn_decode_paged_weights(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(kv_lens),
-                                       _ptr(out), _ptr(lse), _ptr(weight_sums), _ptr(sums_out), B, max_blocks,
-                                       num_pages, Hq, Hkv, D, P, float(scale), float(decay), int(num_splits), _dt(q),
-                                       _ptr(workspace), wsz, _ptr(err_flag), _stream(stream))
+    ws_ptr = None if workspace is None else need(workspace, "workspace", dev, None, None)
+    st = _pycall.attn_decode_paged_weights(
+        q_ptr, need(k_pages, "k_pages", dev, dtype, None), need(v_pages, "v_pages", dev, dtype, k_pages.shape),
+        need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
+        need(kv_lens, "kv_lens", dev, torch.int32, (B,)), need(out, "out", dev, dtype, (B, Hq, D)),
+        need(lse, "lse", dev, torch.float32, (B, Hq)), in_ptr, out_ptr, B, max_blocks, num_pages, Hq, Hkv, D, P, scale,
+        decay, num_splits, _dt(q), ws_ptr, 0 if workspace is None else workspace.nbytes, _ptr(err_flag),
+        _stream(stream))
     _check(st, "attn_decode_paged_weights")
     return out, lse, sums_out
 
@@ -508,23 +509,24 @@ def chunk_weights(q, k_pages, block_table, prefix_lens, lse, weight_sums, scale,
     ``attn_chunk_weights``. ``lse`` ``[B, Hq, C]`` is ``prefill_paged_chunk``'s. Returns the sums."""
     B, C, Hq, D = q.shape
     num_pages, Hkv, P, D2 = k_pages.shape
-    assert D2 == D
+    if D2 != D:
+        raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
     max_blocks = block_table.shape[1]
-    _need(q, "q")
-    _here(q, "q")
-    _need(k_pages, "k_pages", q.dtype)
-    _need(block_table, "block_table", torch.int32, (B, max_blocks))
-    _need(prefix_lens, "prefix_lens", torch.int32, (B,))
-    if chunk_lens is not None:
-        _need(chunk_lens, "chunk_lens", torch.int32, (B,))
-    _need(lse, "lse", torch.float32, (B, Hq, C))
-    _need(weight_sums, "weight_sums", torch.float32, (B, Hkv, max_blocks * P))
+    dev, dtype, need = torch.cuda.current_device() if q.is_cuda else -2, q.dtype, _fast_need
+    q_ptr = need(q, "q", dev, None, None)
+    sums = (B, Hkv, max_blocks * P)
+    in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, torch.float32, sums)
     if sums_out is None:
         sums_out = weight_sums
-    _need(sums_out, "sums_out", torch.float32, weight_sums.shape)
-    st = lib.attn_chunk_weights(_ptr(q), _ptr(k_pages), _ptr(block_table), _ptr(prefix_lens), _ptr(chunk_lens),
-                                _ptr(lse), _ptr(weight_sums), _ptr(sums_out), B, C, int(window), max_blocks, num_pages,
-                                Hq, Hkv, D, P, float(scale), float(decay), _dt(q), _ptr(err_flag), _stream(stream))
+    else:
+        out_ptr = need(sums_out, "sums_out", dev, torch.float32, sums)
+    st = _pycall.attn_chunk_weights(
+        q_ptr, need(k_pages, "k_pages", dev, dtype, None),
+        need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
+        need(prefix_lens, "prefix_lens", dev, torch.int32, (B,)),
+        None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, torch.int32, (B,)),
+        need(lse, "lse", dev, torch.float32, (B, Hq, C)), in_ptr, out_ptr, B, C, window, max_blocks, num_pages, Hq, Hkv,
+        D, P, scale, decay, _dt(q), _ptr(err_flag), _stream(stream))
     _check(st, "attn_chunk_weights")
     return sums_out
 
@@ -536,27 +538,23 @@ def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_t
     num_pages, Hkv, P, D = k_pages.shape
     B, max_blocks = block_table.shape
     new_blocks = new_block_table.shape[1]
-    _need(k_pages, "k_pages")
-    _here(k_pages, "k_pages")
-    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
-    _need(block_table, "block_table", torch.int32)
-    _need(kv_lens, "kv_lens", torch.int32, (B,))
-    _need(weight_sums, "weight_sums", torch.float32, (B, Hkv, max_blocks * P))
-    _need(new_block_table, "new_block_table", torch.int32, (B, new_blocks))
-    budget = int(budget)
+    dev, need = torch.cuda.current_device() if k_pages.is_cuda else -2, _fast_need
+    i32, f32 = torch.int32, torch.float32
+    k_ptr = need(k_pages, "k_pages", dev, None, None)
     if kept is None:
-        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=k_pages.device)
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=i32, device=k_pages.device)
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=k_pages.device)
+        new_lens = torch.empty((B,), dtype=i32, device=k_pages.device)
     if new_sums is None:
-        new_sums = torch.empty((B, Hkv, new_blocks * P), dtype=torch.float32, device=k_pages.device)
-    _need(kept, "kept", torch.int32, (B, Hkv, budget))
-    _need(new_lens, "new_lens", torch.int32, (B,))
-    _need(new_sums, "new_sums", torch.float32, (B, Hkv, new_blocks * P))
-    st = lib.attn_cache_evict(_ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(kv_lens), _ptr(weight_sums),
-                              _ptr(new_block_table), _ptr(kept), _ptr(new_lens), _ptr(new_sums), B, max_blocks,
-                              new_blocks, num_pages, Hkv, D, P, budget, int(n_sink), int(n_recent), _dt(k_pages),
-                              _ptr(err_flag), _stream(stream))
+        new_sums = torch.empty((B, Hkv, new_blocks * P), dtype=f32, device=k_pages.device)
+    st = _pycall.attn_cache_evict(
+        k_ptr, need(v_pages, "v_pages", dev, k_pages.dtype, k_pages.shape),
+        need(block_table, "block_table", dev, i32, None), need(kv_lens, "kv_lens", dev, i32, (B,)),
+        need(weight_sums, "weight_sums", dev, f32, (B, Hkv, max_blocks * P)),
+        need(new_block_table, "new_block_table", dev, i32, (B, new_blocks)),
+        need(kept, "kept", dev, i32, (B, Hkv, max(budget, 0))), need(new_lens, "new_lens", dev, i32, (B,)),
+        need(new_sums, "new_sums", dev, f32, (B, Hkv, new_blocks * P)), B, max_blocks, new_blocks, num_pages, Hkv, D, P,
+        budget, n_sink, n_recent, _dt(k_pages), _ptr(err_flag), _stream(stream))
     _check(st, "attn_cache_evict")
     return kept, new_lens, new_sums
 
@@ -571,20 +569,17 @@ def linear(x, w, bias=None, activation="none", residual=None, out=None, err_flag
     bf16; ``activation`` one of ``ACTIVATIONS``. ``out`` may be ``residual``."""
     m, k = x.shape
     n = w.shape[0]
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}, one of {sorted(ACTIVATIONS)}")
-    _need(x, "x")
-    _here(x, "x")
-    _need(w, "w", x.dtype, (n, k))
-    if bias is not None:
-        _need(bias, "bias", x.dtype, (n,))
-    if residual is not None:
-        _need(residual, "residual", x.dtype, (m, n))
+    dev, dtype, need = torch.cuda.current_device() if x.is_cuda else -2, x.dtype, _fast_need
+    x_ptr = need(x, "x", dev, None, None)
     if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-    _need(out, "out", x.dtype, (m, n))
-    st = lib.attn_linear(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(out), m, n, k, ACTIVATIONS[activation],
-                         _dt(x), _ptr(err_flag), _stream(stream))
+        out = torch.empty((m, n), dtype=dtype, device=x.device)
+    st = _pycall.attn_linear(
+        x_ptr, need(w, "w", dev, dtype, (n, k)), None if bias is None else need(bias, "bias", dev, dtype, (n,)),
+        None if residual is None else need(residual, "residual", dev, dtype, (m, n)), need(out, "out", dev, dtype, (m, n)),
+        m, n, k, act, _dt(x), _ptr(err_flag), _stream(stream))
     _check(st, "attn_linear")
     return out
 

@@ -3,7 +3,8 @@
 Each ``csrc/*.cu`` file compiles to an object in parallel, then one link step
 makes the library. The CUDA runtime is linked statically, and nothing links
 against the driver library, so the library also loads on a machine without a
-GPU (for the export checks). Run ``python -m paged_kv_attention_28_gb300.build``.
+GPU (for the export checks). ``csrc/pycall.c`` becomes ``_pycall.so``, the CPython
+module of the binding's small calls, linked against the library. Run ``python -m paged_kv_attention_28_gb300.build``.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpkvattn.so")
+PYCALL = os.path.join(PKG, "_pycall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -39,10 +42,10 @@ def _flags(verbose_ptxas: bool):
 
 
 def _needs_rebuild(srcs) -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(PYCALL):
         return True
-    t = os.path.getmtime(LIB)
-    deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
+    deps = srcs + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -78,6 +81,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    tmp = PYCALL + ".tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "pycall.c"), "-o", tmp, "-L", PKG, "-l:libpkvattn.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("the Python module's build failed")
+    os.replace(tmp, PYCALL)
     if not quiet:
         print(f"built {LIB}")
     return LIB

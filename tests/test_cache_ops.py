@@ -22,6 +22,7 @@ def b():
 
 P = ctypes.c_void_p(1 << 20)
 ODD = ctypes.c_void_p((1 << 20) + 4)
+ODD1 = ctypes.c_void_p((1 << 20) + 1)
 
 
 # ------------------------------------------------------------------------------------ the oracle
@@ -195,3 +196,48 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(b):
         b.linear(q[0, 0], q[0, 0], activation="tanh")
     with pytest.raises(ValueError):
         b.cache_evict(kp, kp, i, n, torch.zeros(1, 2, 64), i, 16)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only where nothing can be launched")
+def test_native_calls_take_what_ctypes_takes(b):
+    """The module's wrappers pass every argument on in its place: the same refusals as through
+    ctypes, one argument at a time, and sizes past 32 bits do not wrap."""
+    from paged_kv_attention_28_gb300 import _pycall
+    for name, good in (("attn_qk_norm_rope_append", append_args(b, qn=P, kn=P)),
+                       ("attn_decode_paged_weights", weights_args(b, lse=P, wsz=0)), ("attn_chunk_weights", chunk_args(b, cl=P)),
+                       ("attn_cache_evict", evict_args(b)), ("attn_linear", linear_args(b, bias=ODD1, res=P))):
+        call, ref = getattr(_pycall, name), getattr(b.lib, name)
+        raw = lambda args: [x.value if isinstance(x, ctypes.c_void_p) else x for x in args]  # noqa: E731
+        assert call(*raw(good)) == ref(*good), name
+        for i, x in enumerate(good):
+            if x is None:
+                continue
+            size = name == "attn_decode_paged_weights" and i == 21  # (a size_t: no negative values)
+            for bad in (5, 1 << 40) if size else (None, ODD1) if isinstance(x, ctypes.c_void_p) else (float("nan"),) if isinstance(x, float) else (-7, 5, 0):
+                args = good[:i] + [bad] + good[i + 1:]
+                assert call(*raw(args)) == ref(*args), (name, i, bad)
+            wide = isinstance(x, int) and not (name == "attn_qk_norm_rope_append" and 3 <= i <= 5)
+            if wide and not size:
+                assert call(*raw(good[:i] + [(1 << 32) + x] + good[i + 1:])) == b.PKV_ERR_INVALID_ARG, (name, i)
+        with pytest.raises(TypeError):
+            call(*raw(good[:-1]))
+        with pytest.raises(TypeError):
+            call("x", *raw(good[1:]))
+
+
+def test_need_checks_a_tensor(b):
+    from paged_kv_attention_28_gb300 import _pycall
+    class T:
+        dtype, shape = torch.int32, torch.Size((2, 3))
+        get_device = staticmethod(lambda: 0)
+        is_contiguous = staticmethod(lambda: True)
+        data_ptr = staticmethod(lambda: 4096)
+    assert _pycall.need(T, "t", 0, torch.int32, (2, 3)) == 4096 and _pycall.need(T, "t", 0, None, None) == 4096
+    for bad in ((1, torch.int32, (2, 3)), (0, torch.int64, (2, 3)), (0, torch.int32, (3, 2)), (0, torch.int32, (2,))):
+        with pytest.raises(ValueError):
+            _pycall.need(T, "t", *bad)
+    with pytest.raises(ValueError, match="t must be a CUDA tensor"):
+        _pycall.need(torch.zeros(2), "t", 0, None, None)
+    T.is_contiguous = staticmethod(lambda: False)
+    with pytest.raises(ValueError, match="contiguous"):
+        _pycall.need(T, "t", 0, None, None)
