@@ -9,19 +9,24 @@
 // thread owns one key, i.e. one TMEM lane, so a key's sum over the columns never leaves its
 // thread: no reduction across threads, and a fixed order of additions.
 //
-// Bound: one exponential per (key, query, head). The special-function unit gives 16 a clock and
-// SM, 2048 clocks for a 256 x 128 step, and the two products of a step take about 1750 (128 x 128
-// products read both operands from shared memory, which is their limit). So a quarter of the
-// exponentials are computed as polynomials on the FMA units instead, which leaves the special-
-// function unit 1536 clocks and puts the products on the critical path.
+// Bound: per 256 x 128 step the special-function unit needs 2048 clocks at 16 exponentials a clock
+// and SM, the two products 1024, which read 128 bytes a clock of shared memory all that time, and the
+// columns' log-sum-exps are read from there too. Measured 1090 ns (about 2070 clocks) a step: the
+// prompt chunk of 2048 queries over 2 x 3-4k keys, 32 heads on 8, takes 92 us. Tried and not kept: a
+// share of the exponentials as polynomials on the FMA units (12 % slower for each eighth: the issue
+// slots are not free), eight exponential warps for sixteen (14 % slower), one warp issuing the
+// products of both tiles (the tensor cores idle while it waits), two-wide fp32 arithmetic.
+// With a window of few queries an item is a single step, and what bounds it is the chain of
+// barriers, loads and address arithmetic around the step, about 2.8 us of a CTA an item.
 //
 // A persistent CTA per SM takes items (sequence, KV head, 256 keys) in an order that pairs long and
 // short ones: key tiles slowest (early keys are seen by the most queries), and every other round
-// of the CTAs backwards. With fewer items than half the SMs an item's steps are shared by a
-// cluster of 2 to 8 CTAs, whose partial sums are added in rank order through distributed shared memory.
-// Warps: 0 TMA producer (K tiles by page, two items deep; Q tiles, three deep), 1 MMA issuer, 2 the
-// columns' log-sum-exps into shared memory, 4..7 and 8..11 the two key tiles' exponentials and
-// sums. S^T is double-buffered per tile: all 512 TMEM columns.
+// of the CTAs backwards (135 to 108 us against a plain stride). With fewer items than half the SMs
+// an item's steps are shared by a cluster of 2 to 8 CTAs, whose partial sums are added in rank
+// order through distributed shared memory.
+// Warps: 0 and 2 TMA producers (a ring of three K tiles, page by page, and one of three Q tiles), 1
+// and 3 MMA issuers of the two key tiles, 4..11 and 12..19 their exponentials and sums. S^T is
+// double-buffered per tile: all 512 TMEM columns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -40,14 +45,21 @@ namespace {
 constexpr int CD = 128;                // head dim
 constexpr int CK = 256;                // keys per item: two 128-row tiles
 constexpr int CN = 128;                // columns (queries x heads of the group) per step
-constexpr int KSTG = CK * CD * 2;      // one K stage, 64 KiB: tile 0 halves, tile 1 halves
+// One K stage, 32 KiB: 8-row groups of 2 KiB, each its two 64-dim halves of [8 rows][128 bytes], so
+// that a page (16 rows of 256 bytes, contiguous in the pool) is one box and the groups of all pages
+// lie at one distance.
+constexpr int KSTG = 128 * CD * 2;
 constexpr int QSTG = CN * CD * 2;      // one Q stage, 32 KiB: two 64-dim halves
 constexpr int HALF = 128 * 128;        // [128 rows][128 bytes]
-constexpr int NKS = 2, NQS = 3;
-constexpr int CTHREADS = 384;
+constexpr int NKS = 3, NQS = 3;
+constexpr int CTHREADS = 640;
 // barriers
-constexpr int C_KF = 0, C_KE = 2, C_QF = 4, C_QE = 7, C_LF = 10, C_LE = 13, C_SF = 16, C_SE = 20, C_DR = 24, C_NBAR = 25;
-constexpr int SM_K = 0, SM_Q = SM_K + NKS * KSTG, SM_L = SM_Q + NQS * QSTG, SM_BAR = SM_L + NQS * CN * 4,
+constexpr int C_KF = 0, C_KE = 3, C_QF = 6, C_QE = 9, C_SF = 12, C_SE = 16, C_DR = 20, C_HF = 21,
+              C_NBAR = C_HF + 8 * 3;
+constexpr int CLENS = 2048;            // sequences whose lengths are kept in shared memory
+constexpr int CWARPS = 16;             // exponential warps, four .. nineteen
+constexpr int SM_K = 0, SM_Q = SM_K + NKS * KSTG, SM_L = SM_Q + NQS * QSTG, SM_X = SM_L + CWARPS * CN * 4, SM_LEN = SM_X + 4 * CK * 4,
+              SM_BAR = SM_LEN + CLENS * 8,
               SM_MISC = SM_BAR + C_NBAR * 8, C_SMEM = SM_MISC + 16 + 1024;
 static_assert(C_SMEM <= 232448, "shared memory per CTA");
 constexpr float kL2e = 1.4426950408889634f;
@@ -93,112 +105,51 @@ struct Cursor {
   }
 };
 
-__device__ __forceinline__ Item make_item(const ChunkWeightsArgs& a, const Cursor& c, int qpt_log2) {
+// A sequence's cached and new tokens; the new ones are -1 where the lengths are bad.
+__device__ __forceinline__ int2 read_lens(const ChunkWeightsArgs& a, int b) {
+  const int64_t prefix = __ldg(a.prefix_lens + b);
+  const int64_t n = a.chunk_lens ? __ldg(a.chunk_lens + b) : a.chunk_len;
+  const bool bad = prefix < 0 || n < 0 || n > a.chunk_len || prefix + n > (int64_t)a.max_blocks * a.page_size;
+  return make_int2((int)prefix, bad ? -1 : (int)n);
+}
+
+__device__ __forceinline__ Item make_item(const ChunkWeightsArgs& a, const int2* lens, const Cursor& c, int qpt_log2) {
   Item it{};
   it.key0 = c.tile * CK;
   it.b = c.b;
   it.hk = c.hk;
-  const int64_t prefix = __ldg(a.prefix_lens + it.b);
-  const int64_t n = a.chunk_lens ? __ldg(a.chunk_lens + it.b) : a.chunk_len;
-  const int64_t cap = (int64_t)a.max_blocks * a.page_size;
-  if (prefix < 0 || n < 0 || n > a.chunk_len || prefix + n > cap) {
+  const int2 len = c.b < CLENS ? lens[c.b] : read_lens(a, c.b);
+  const int prefix = len.x, n = len.y;
+  if (n < 0) {
     it.total = -1;
     return it;
   }
-  it.total = (int)(prefix + n);
-  it.prefix = (int)prefix;
+  it.total = prefix + n;
+  it.prefix = prefix;
   if (it.key0 >= it.total) {
     it.total = 0;
     return it;
   }
-  const int first = a.window > 0 && a.window < n ? (int)n - a.window : 0;
+  const int first = a.window > 0 && a.window < n ? n - a.window : 0;
   it.q_begin = max(first, it.key0 - it.prefix);
-  it.q_end = (int)n;
+  it.q_end = n;
   it.steps = it.q_end > it.q_begin ? (it.q_end - it.q_begin + (1 << qpt_log2) - 1) >> qpt_log2 : 0;
   return it;
 }
 
-__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 upk2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// 2^x of a pair without the special-function unit, x <= 0: x = n + f with n the nearest integer
-// (adding 1.5 * 2^23 leaves it in the low bits), 2^f on [-1/2, 1/2] as the degree-5 polynomial of
-// least relative error (2e-7 with its fp32 roundings; the exponent unit's is 1e-7), times 2^n
-// made from n's bits. Below -126 it stays at 2^-126; NaN stays NaN.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
-  constexpr float kRound = 12582912.0f;
-  const float2 x = upk2(x2);
-  const uint64_t y = pk2(max_nan(x.x, -126.0f), max_nan(x.y, -126.0f));
-  const uint64_t t = fadd2(y, pk2(kRound, kRound));
-  const uint64_t n = fadd2(t, pk2(-kRound, -kRound));
-  const uint64_t f = ffma2(n, pk2(-1.0f, -1.0f), y);
-  uint64_t p = pk2(0.0013276472f, 0.0013276472f);
-  p = ffma2(p, f, pk2(0.009675541f, 0.009675541f));
-  p = ffma2(p, f, pk2(0.05550713f, 0.05550713f));
-  p = ffma2(p, f, pk2(0.2402212f, 0.2402212f));
-  p = ffma2(p, f, pk2(0.69314694f, 0.69314694f));
-  p = ffma2(p, f, pk2(1.0f, 1.0f));
-  const float2 b = upk2(t);
-  return fmul2(p, pk2(__uint_as_float((__float_as_uint(b.x) << 23) + 0x3f800000u),
-                      __uint_as_float((__float_as_uint(b.y) << 23) + 0x3f800000u)));
-}
-
 // acc += exp2(s * c + nl) over 32 columns; MASKED: columns outside [lo, hi) do not count.
 template <bool MASKED>
-__device__ __forceinline__ void add_columns(const uint32_t (&s)[32], const float* nl, uint64_t c2, int col0, int lo,
-                                            int hi, uint64_t (&acc)[2]) {
+__device__ __forceinline__ void add_columns(const uint32_t (&s)[32], const float* nl, float c, int col0, int lo, int hi,
+                                            float (&acc)[4]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    uint64_t e[4];
-#pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-      const ulonglong2 n = *reinterpret_cast<const ulonglong2*>(nl + i + 2 * k);
-      e[k] = ffma2(pk2(__uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1])), c2, n.x);
-      e[k + 1] = ffma2(pk2(__uint_as_float(s[i + 2 * k + 2]), __uint_as_float(s[i + 2 * k + 3])), c2, n.y);
-    }
+  for (int i = 0; i < 32; i += 4) {
+    const float4 n4 = *reinterpret_cast<const float4*>(nl + i);
+    const float n[4] = {n4.x, n4.y, n4.z, n4.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (k == 3) {
-        e[k] = exp2_poly2(e[k]);
-      } else {
-        const float2 x = upk2(e[k]);
-        e[k] = pk2(ex2(x.x), ex2(x.y));
-      }
-      if (MASKED) {
-        const float2 x = upk2(e[k]);
-        const int c = col0 + i + 2 * k;
-        e[k] = pk2(c >= lo && c < hi ? x.x : 0.0f, c + 1 >= lo && c + 1 < hi ? x.y : 0.0f);
-      }
-      acc[k & 1] = fadd2(acc[k & 1], e[k]);
+      float e = ex2(fmaf(__uint_as_float(s[i + k]), c, n[k]));
+      if (MASKED) e = col0 + i + k >= lo && col0 + i + k < hi ? e : 0.0f;
+      acc[k] += e;
     }
   }
 }
@@ -213,7 +164,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 template <bool SPLIT>
 __global__ void __launch_bounds__(CTHREADS, 1)
 chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const ChunkWeightsArgs a, int n_tiles, int S) {
+                     const ChunkWeightsArgs a, int n_tiles, int s_log2) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
@@ -225,14 +176,20 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   const int G = a.n_qo_heads / a.n_kv_heads;  // a power of two
   const int g_log2 = 31 - __clz(G), qpt_log2 = 7 - g_log2, qpt = 1 << qpt_log2;  // queries per step
   static_assert(CN == 128, "qpt_log2");
+  const int S = SPLIT ? 1 << s_log2 : 1;
   const int rank = SPLIT ? (int)cluster_rank() : 0;  // steps rank, rank + S, ... of the CTA's items
-  const int cta = SPLIT ? (int)blockIdx.x / S : (int)blockIdx.x, ctas = SPLIT ? (int)gridDim.x / S : (int)gridDim.x;
+  const int cta = SPLIT ? (int)blockIdx.x >> s_log2 : (int)blockIdx.x;
+  const int ctas = SPLIT ? (int)gridDim.x >> s_log2 : (int)gridDim.x;
+  // steps of an item that this CTA takes
+  auto share_of = [&](int steps) { return SPLIT ? (steps > rank ? (steps - rank + S - 1) >> s_log2 : 0) : steps; };
 
+  int2* lens = reinterpret_cast<int2*>(smem + SM_LEN);
+  for (int b = threadIdx.x; b < a.batch && b < CLENS; b += CTHREADS) lens[b] = read_lens(a, b);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C_NBAR; ++i) {
       int cnt = 1;
-      if (i >= C_SE && i < C_SE + 4) cnt = 4;  // the four warps of a key tile
-      if (i >= C_LE && i < C_LE + NQS) cnt = 8;  // all eight
+      if (i >= C_SE && i < C_SE + 4) cnt = 4;  // the four warps that read the buffer
+      if ((i >= C_QE && i < C_QE + NQS) || i == C_DR) cnt = 2;  // both issuers
       mbar_init(bar(i), cnt);
     }
     misc->abort_ = 0;
@@ -254,11 +211,13 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     }
   };
 
-  // One key of an item: where its sum is, the old sum, and whether its page exists.
+  // One key of an item: where its sum is, the old sum and its table entry (neither is looked at
+  // before the end of the item, when the loads are long done).
   struct Mine {
     int64_t at;
     float before;
-    bool live, bad_page;
+    int page;
+    bool live;
   };
   auto my_key = [&](const Item& it, int t) {
     Mine m{};
@@ -267,274 +226,267 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     if (m.live) {
       m.at = ((int64_t)it.b * a.n_kv_heads + it.hk) * ((int64_t)a.max_blocks * a.page_size) + key;
       m.before = a.sums_in[m.at];
-      const int page = __ldg(a.block_table + (int64_t)it.b * a.max_blocks + key / 16);
-      m.bad_page = page < 0 || page >= a.num_pages;
+      m.page = __ldg(a.block_table + (int64_t)it.b * a.max_blocks + key / 16);
     }
     return m;
   };
   auto store = [&](const Mine& m, float total) {
-    if (m.bad_page) set_err(a.err_flag, PKV_DEVERR_BAD_PAGE);
-    a.sums_out[m.at] = m.bad_page ? NAN : fmaf(a.decay, m.before, total);
+    const bool bad = m.page < 0 || m.page >= a.num_pages;
+    if (bad) set_err(a.err_flag, PKV_DEVERR_BAD_PAGE);
+    a.sums_out[m.at] = bad ? NAN : fmaf(a.decay, m.before, total);
   };
-  float part = 0.0f;  // SPLIT: this CTA's share of a key's sum
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    if (elect_one()) {
-      tma_prefetch_desc(&mq);
-      tma_prefetch_desc(&mk);
-    }
-    __syncwarp();
-    uint32_t kc = 0, qc = 0;
-    bool ok = true;
-    // lane p < 16 holds the table entry of page p of the item; slots past the sequence bring its
-    // first page again (their keys are not written), a bad entry page 0 (its keys become NaN).
-    // The next item's entries are asked for before this item's copies wait for room.
-    auto entry = [&](const Item& it) {
-      const int pages = min(CK / 16, (it.total - it.key0 + 15) / 16);
-      return lane < 16 && it.steps > 0
-                 ? __ldg(a.block_table + (int64_t)it.b * a.max_blocks + it.key0 / 16 + (lane < pages ? lane : 0))
-                 : 0;
-    };
-    Cursor at(a, cta, ctas);
-    Item next{};
-    int next_phys = 0;
-    bool more = at.tile < n_tiles;
-    if (more) {
-      next = make_item(a, at, qpt_log2);
-      next_phys = entry(next);
-    }
-    while (ok && more) {
-      const Item it = next;
-      int phys = next_phys;
-      at.next(a);
-      more = at.tile < n_tiles;
+  // Registers: 96 a thread at launch; the first warpgroup gives 32 each to the four with the
+  // exponentials, 8 more each there (every warp of a warpgroup takes the same setmaxnreg).
+  static_assert(128 * 64 + 512 * 104 <= CTHREADS * 96, "register split");
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+    if (warp == 0) {
+      // ------------------------------------------------------------------ TMA producer of K tiles
+      if (elect_one()) tma_prefetch_desc(&mk);
+      __syncwarp();
+      uint32_t kc = 0;
+      bool ok = true;
+      // lane p < 16 holds the table entry of page p of the item; slots past the sequence bring its
+      // first page again (their keys are not written), a bad entry page 0 (its keys become NaN).
+      // The next item's entries are asked for before this item's copies wait for room.
+      auto entry = [&](const Item& it) {
+        const int pages = min(CK / 16, (it.total - it.key0 + 15) / 16);
+        return lane < 16 && it.steps > 0
+                   ? __ldg(a.block_table + (int64_t)it.b * a.max_blocks + it.key0 / 16 + (lane < pages ? lane : 0))
+                   : 0;
+      };
+      Cursor at(a, cta, ctas);
+      Item next{};
+      int next_phys = 0;
+      bool more = at.tile < n_tiles;
       if (more) {
-        next = make_item(a, at, qpt_log2);
+        next = make_item(a, lens, at, qpt_log2);
         next_phys = entry(next);
       }
-      if (it.steps == 0) continue;
-      const uint32_t ks = kc % NKS;
-      if (kc >= NKS && !warp_wait(bar(C_KE + ks), (kc / NKS - 1) & 1)) ok = false;
-      if (__any_sync(0xffffffffu, *aborted)) ok = false;
-      if (!ok) break;
-      if (phys < 0 || phys >= a.num_pages) phys = 0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(bar(C_KF + ks), KSTG);
-      __syncwarp();
-      if (lane < 16) {
-        const uint32_t dst = sb + SM_K + ks * KSTG + (lane >> 3) * 2 * HALF + (lane & 7) * 2048;
-        const int row = (phys * a.n_kv_heads + it.hk) * 16;
-        tma_load_2d(dst, &mk, 0, row, bar(C_KF + ks));
-        tma_load_2d(dst + HALF, &mk, 64, row, bar(C_KF + ks));
-      }
-      __syncwarp();
-      ++kc;
-      for (int s = rank; s < it.steps; s += S, ++qc) {
-        const uint32_t qs = qc % NQS;
-        if (qc >= NQS && !warp_wait(bar(C_QE + qs), (qc / NQS - 1) & 1)) ok = false;
-        if (__any_sync(0xffffffffu, *aborted)) ok = false;
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(bar(C_QF + qs), QSTG);
-          const uint32_t dst = sb + SM_Q + qs * QSTG;
-          tma_load_4d(dst, &mq, 0, it.hk * G, it.q_begin + s * qpt, it.b, bar(C_QF + qs));
-          tma_load_4d(dst + HALF, &mq, 64, it.hk * G, it.q_begin + s * qpt, it.b, bar(C_QF + qs));
+      while (ok && more) {
+        const Item it = next;
+        int phys = next_phys;
+        at.next(a);
+        more = at.tile < n_tiles;
+        if (more) {
+          next = make_item(a, lens, at, qpt_log2);
+          next_phys = entry(next);
         }
-        __syncwarp();
-      }
-    }
-    if (!ok) give_up();
-    // every issued copy lands before the shared memory is released
-    bool drained = true;
-    for (uint32_t s = 0; s < NKS && s < kc; ++s)
-      drained &= warp_wait(bar(C_KF + s), ((kc - 1 - s) / NKS) & 1);
-    for (uint32_t s = 0; s < NQS && s < qc; ++s)
-      drained &= warp_wait(bar(C_QF + s), ((qc - 1 - s) / NQS) & 1);
-    if (!drained) give_up();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
-    const uint32_t idesc = idesc_bf16_f32(128, CN, false, false);
-    const uint64_t dk0 = smem_desc(sb + SM_K, 16, 1024, kSwizzle128B);
-    const uint64_t dq0 = smem_desc(sb + SM_Q, 16, 1024, kSwizzle128B);
-    uint32_t kc = 0, qc = 0;
-    bool ok = true;
-    for (Cursor at(a, cta, ctas); ok && at.tile < n_tiles; at.next(a)) {
-      const Item it = make_item(a, at, qpt_log2);
-      if (it.steps == 0) continue;
-      const uint32_t ks = kc % NKS;
-      if (!warp_wait(bar(C_KF + ks), (kc / NKS) & 1)) ok = false;
-      for (int s = rank; ok && s < it.steps; s += S, ++qc) {
-        const uint32_t qs = qc % NQS, buf = qc & 1;
-        if (!warp_wait(bar(C_QF + qs), (qc / NQS) & 1)) {
+        if (it.steps == 0) continue;
+        if (__any_sync(0xffffffffu, *aborted)) {
           ok = false;
           break;
         }
-        for (int tile = 0; ok && tile < 2; ++tile) {
-          if (qc >= 2 && !warp_wait(bar(C_SE + 2 * tile + buf), (qc / 2 - 1) & 1)) {
-            ok = false;
-            break;
+        if (phys < 0 || phys >= a.num_pages) phys = 0;
+        for (int tile = 0; ok && tile < 2; ++tile, ++kc) {  // lanes 8 tile .. 8 tile + 7 hold its pages
+          const uint32_t ks = kc % NKS;
+          if (kc >= NKS && !warp_wait(bar(C_KE + ks), (kc / NKS - 1) & 1)) ok = false;
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(C_KF + ks), KSTG);
+          __syncwarp();
+          if ((lane >> 3) == tile)
+            tma_load_4d(sb + SM_K + ks * KSTG + (lane & 7) * 4096, &mk, 0, 0, 0, (phys * a.n_kv_heads + it.hk) * 2,
+                        bar(C_KF + ks));
+          __syncwarp();
+        }
+      }
+      if (!ok) give_up();
+      // every issued copy lands before the shared memory is released
+      bool drained = true;
+      for (uint32_t s = 0; s < NKS && s < kc; ++s) drained &= warp_wait(bar(C_KF + s), ((kc - 1 - s) / NKS) & 1);
+      if (!drained) give_up();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------------ TMA producer of Q tiles
+      if (elect_one()) tma_prefetch_desc(&mq);
+      __syncwarp();
+      uint32_t qc = 0;
+      bool ok = true;
+      for (Cursor at(a, cta, ctas); ok && at.tile < n_tiles; at.next(a)) {
+        const Item it = make_item(a, lens, at, qpt_log2);
+        if (__any_sync(0xffffffffu, *aborted)) ok = false;
+        for (int s = rank; ok && s < it.steps; s += S, ++qc) {
+          const uint32_t qs = qc % NQS;
+          if (qc >= NQS && !warp_wait(bar(C_QE + qs), (qc / NQS - 1) & 1)) ok = false;
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar(C_QF + qs), QSTG);
+            const uint32_t dst = sb + SM_Q + qs * QSTG;
+            tma_load_4d(dst, &mq, 0, it.hk * G, it.q_begin + s * qpt, it.b, bar(C_QF + qs));
+            tma_load_4d(dst + HALF, &mq, 64, it.hk * G, it.q_begin + s * qpt, it.b, bar(C_QF + qs));
           }
+          __syncwarp();
+        }
+      }
+      if (!ok) give_up();
+      bool drained = true;
+      for (uint32_t s = 0; s < NQS && s < qc; ++s) drained &= warp_wait(bar(C_QF + s), ((qc - 1 - s) / NQS) & 1);
+      if (!drained) give_up();
+    } else if (warp == 1 || warp == 3) {
+      // ------------------------------------------------------------------ MMA issuers
+      // One warp per key tile: while one waits for its barriers, the other's products run.
+      const int tile = warp >> 1;
+      const uint32_t idesc = idesc_bf16_f32(128, CN, false, false);
+      const uint64_t dk0 = smem_desc(sb + SM_K, 16, 2048, kSwizzle128B);
+      const uint64_t dq0 = smem_desc(sb + SM_Q, 16, 1024, kSwizzle128B);
+      uint32_t kt = tile, qc = 0;  // this tile's place in the K ring, steps so far
+      bool ok = true;
+      for (Cursor at(a, cta, ctas); ok && at.tile < n_tiles; at.next(a)) {
+        const Item it = make_item(a, lens, at, qpt_log2);
+        if (it.steps == 0) continue;
+        const uint32_t ks = kt % NKS;
+        const uint64_t dk = dk0 + (uint64_t)((ks * KSTG) >> 4);
+        for (int s = rank; ok && s < it.steps; s += S, ++qc) {
+          const uint32_t qs = qc % NQS, buf = qc & 1;
+          if (s == rank && !warp_wait(bar(C_KF + ks), (kt / NKS) & 1)) ok = false;
+          if (ok && !warp_wait(bar(C_QF + qs), (qc / NQS) & 1)) ok = false;
+          if (ok && qc >= 2 && !warp_wait(bar(C_SE + 2 * tile + buf), (qc / 2 - 1) & 1)) ok = false;
+          if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t dk = dk0 + (uint64_t)((ks * KSTG + tile * 2 * HALF) >> 4);
             const uint64_t dq = dq0 + (uint64_t)((qs * QSTG) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < CD / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk / 4) * HALF + (kk % 4) * 32) >> 4);
-              mma_bf16_ss(tmem + (2 * tile + buf) * CN, dk + off, dq + off, idesc, kk > 0 ? 1u : 0u);
-            }
+  #pragma unroll
+            for (int kk = 0; kk < CD / 16; ++kk)
+              mma_bf16_ss(tmem + (2 * tile + buf) * CN, dk + (uint64_t)(((kk / 4) * 1024 + (kk % 4) * 32) >> 4),
+                          dq + (uint64_t)(((kk / 4) * HALF + (kk % 4) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
             mma_commit(bar(C_SF + 2 * tile + buf));
-            if (tile == 1) {
-              mma_commit(bar(C_QE + qs));
-              if (s + S >= it.steps) mma_commit(bar(C_KE + ks));
-            }
+            mma_commit(bar(C_QE + qs));
+            if (s + S >= it.steps) mma_commit(bar(C_KE + ks));
           }
           __syncwarp();
         }
+        kt += 2;
       }
-      ++kc;
+      if (!ok) give_up();
+      // every issued product finishes before TMEM is freed
+      if (elect_one()) mma_commit(bar(C_DR));
+      __syncwarp();
+      if (!warp_wait(bar(C_DR), 0)) give_up();
     }
-    if (!ok) give_up();
-    // every issued product finishes before TMEM is freed
-    if (elect_one()) mma_commit(bar(C_DR));
-    __syncwarp();
-    if (!warp_wait(bar(C_DR), 0)) give_up();
-  } else if (warp == 2) {
-    // ------------------------------------------------------------------ log-sum-exps
-    // Step after step through the CTA's items; the values of kAhead steps are on their way, since
-    // one step takes less time than one load from the L2.
-    constexpr int kAhead = 4;
-    // the lane's columns: query and place in lse of a step
-    int query[CN / 32];
-    int64_t place[CN / 32];
-#pragma unroll
-    for (int k = 0; k < CN / 32; ++k) {
-      const int col = k * 32 + lane;
-      query[k] = col >> g_log2;
-      place[k] = (int64_t)(col & (G - 1)) * a.chunk_len + query[k];
-    }
-    Cursor at(a, cta, ctas);
-    int s = rank;
-    Item it{};
-    const float* rows = a.lse;
-    auto enter = [&]() {
-      it = make_item(a, at, qpt_log2);
-      s = rank;
-      rows = a.lse + ((int64_t)it.b * a.n_qo_heads + it.hk * G) * a.chunk_len;
-    };
-    if (at.tile < n_tiles) enter();
-    auto load = [&](float (&v)[CN / 32]) -> bool {  // the next step's columns; false: no more steps
-      while (at.tile < n_tiles && s >= it.steps) {
-        at.next(a);
-        if (at.tile < n_tiles) enter();
-      }
-      if (at.tile >= n_tiles) return false;
-      const int q0 = it.q_begin + (s << qpt_log2);
-#pragma unroll
-      for (int k = 0; k < CN / 32; ++k) v[k] = q0 + query[k] < it.q_end ? __ldg(rows + q0 + place[k]) : 0.0f;
-      s += S;
-      return true;
-    };
-    float v[kAhead][CN / 32];
-    bool has[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) has[u] = load(v[u]);
-    uint32_t qc = 0;
-    bool ok = true, more = true;
-    while (ok && more) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (!ok || !has[u]) {
-          more = false;
-          continue;
-        }
-        const uint32_t qs = qc % NQS;
-        if (qc >= NQS && !warp_wait(bar(C_LE + qs), (qc / NQS - 1) & 1)) ok = false;
-        if (__any_sync(0xffffffffu, *aborted)) ok = false;
-        if (ok) {
-          float* dst = reinterpret_cast<float*>(smem + SM_L) + qs * CN;
-#pragma unroll
-          for (int k = 0; k < CN / 32; ++k) dst[k * 32 + lane] = -kL2e * v[u][k];
-          __syncwarp();
-          if (elect_one()) mbar_arrive(bar(C_LF + qs));
-          __syncwarp();
-          ++qc;
-          has[u] = load(v[u]);
-        }
-      }
-    }
-    if (!ok) give_up();
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
     // ------------------------------------------------------------------ exponentials and sums
-    const int tile = (warp - 4) >> 2, wq = warp & 3;
+    // Eight warps per key tile, two for each quarter of its TMEM lanes: `half` 0 takes the even
+    // steps (S buffer 0), 1 the odd ones, so each buffer goes between the products and its own
+    // warps. An item of one step is finished by the warps that take it; of more, by half 0, to
+    // which half 1 hands its sums (three slots: a step of an item in between stands before each reuse).
+    const int tile = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, wq = warp & 3;
+    const int hand_bar = C_HF + (tile * 4 + wq) * 3;
+    float* handed = reinterpret_cast<float*>(smem + SM_X);  // [3][CK]
+    uint32_t n_hand = 0;
     const int t = tile * 128 + wq * 32 + lane;  // key within the item
     const uint32_t lane_addr = (uint32_t)(wq * 32) << 16;
     const float c = a.scale * kL2e;
-    const uint64_t c2 = pk2(c, c);
-    uint32_t qc = 0;
-    bool ok = true;
-    // the next item's lengths, old sum and table entry are asked for before this one's steps
+    // The lane's four columns of a step, whose log-sum-exps it brings to the warp's own corner of
+    // shared memory for all lanes to read; they are asked for one step ahead.
+    constexpr int LC = CN / 32;
+    float* nl = reinterpret_cast<float*>(smem + SM_L) + (warp - 4) * CN;
+    const uint32_t src = tmem + lane_addr + (2 * tile + half) * CN;
+    auto lse_of = [&](const Item& it, int s, float (&v)[LC]) {
+      if (s >= it.steps) return;
+      const int q0 = it.q_begin + (s << qpt_log2);
+      const float* rows = a.lse + ((int64_t)it.b * a.n_qo_heads + it.hk * G) * a.chunk_len + q0;
+#pragma unroll
+      for (int k = 0; k < LC; ++k) {
+        const int col = 32 * k + lane, query = col >> g_log2;
+        v[k] = q0 + query < it.q_end ? __ldg(rows + (int64_t)(col & (G - 1)) * a.chunk_len + query) : 0.0f;
+      }
+    };
+    // look() goes on to the next item that these warps have a part in, and asks for its old sums,
+    // table entries and first log-sum-exps, before the steps of the one at hand.
     Cursor at(a, cta, ctas);
     Item it{};
+    int count = 0;       // steps of the item that are this CTA's
+    uint32_t next_qc = 0;  // steps before it
+    bool more = true, finish = false;
     Mine mine{};
-    bool more = at.tile < n_tiles;
-    if (more) {
-      it = make_item(a, at, qpt_log2);
-      mine = my_key(it, t);
-    }
+    float ahead[LC] = {};
+    auto look = [&]() {
+      for (;; at.next(a)) {
+        next_qc += count;
+        count = 0;
+        more = at.tile < n_tiles;
+        if (!more) return;
+        it = make_item(a, lens, at, qpt_log2);
+        if (it.total <= 0) {
+          if (it.total < 0 && t == 0 && half == 0 && it.key0 == 0 && it.hk == 0) set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
+          continue;
+        }
+        count = share_of(it.steps);
+        if (count != 1 || half == (int)(next_qc & 1)) break;
+      }
+      at.next(a);
+      finish = count == 1 || half == 0;
+      if (finish) mine = my_key(it, t);
+      lse_of(it, rank + (int)((half ^ next_qc) & 1) * S, ahead);
+    };
+    bool ok = true;
+    look();
     while (more) {
       const Item now = it;
       const Mine my = mine;
-      at.next(a);
-      more = at.tile < n_tiles;
-      if (more) {
-        it = make_item(a, at, qpt_log2);
-        mine = my_key(it, t);
-      }
-      if (now.total <= 0) {
-        if (now.total < 0 && t == 0 && now.key0 == 0 && now.hk == 0) set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
-        continue;
-      }
+      const int n_steps = count;
+      const uint32_t qc = next_qc;
+      const bool fin = finish;
+      float v[LC];
+#pragma unroll
+      for (int k = 0; k < LC; ++k) v[k] = ahead[k];
+      look();
       const int key = now.key0 + t;
       float total = 0.0f;
-      for (int s = rank; ok && s < now.steps; s += S, ++qc) {
-        const uint32_t qs = qc % NQS, buf = qc & 1;
-        ok = warp_wait(bar(C_LF + qs), (qc / NQS) & 1) && warp_wait(bar(C_SF + 2 * tile + buf), (qc / 2) & 1);
+      const int mine_first = (int)((half ^ qc) & 1);  // of the item's steps, this half takes every other one
+      for (int k0 = mine_first; ok && k0 < n_steps; k0 += 2) {
+        const int s = rank + k0 * S;
+#pragma unroll
+        for (int k = 0; k < LC; ++k) nl[32 * k + lane] = -kL2e * v[k];
+        __syncwarp();
+        lse_of(now, s + 2 * S, v);
+        ok = warp_wait(bar(C_SF + 2 * tile + half), ((qc + k0) / 2) & 1);
         if (!ok) break;
         tc_fence_after();
-        const float* nl = reinterpret_cast<const float*>(smem + SM_L) + qs * CN;
         const int q0 = now.q_begin + s * qpt;
         // columns [lo, hi) count: the causal bound and the end of the chunk
         const int lo = (key - now.prefix - q0) * G, hi = min(CN, (now.q_end - q0) * G);
-        const uint32_t src = tmem + lane_addr + (2 * tile + buf) * CN;
         const bool whole = __all_sync(0xffffffffu, lo <= 0) && hi == CN;
-        uint64_t acc[2] = {0ull, 0ull};
-        uint32_t r[2][32];
-        tmem_ld32(src, r[0]);
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < CN / 32; ++k) {
+          uint32_t r[32];
+          tmem_ld32(src + 32 * k, r);
           tmem_ld_wait();
-          if (k + 1 < CN / 32) tmem_ld32(src + (k + 1) * 32, r[(k + 1) & 1]);
+          if (k == CN / 32 - 1) {  // the buffer is read: the next products may start
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(bar(C_SE + 2 * tile + half));
+            __syncwarp();
+          }
           if (whole)
-            add_columns<false>(r[k & 1], nl + 32 * k, c2, 32 * k, lo, hi, acc);
+            add_columns<false>(r, nl + 32 * k, c, 32 * k, lo, hi, acc);
           else
-            add_columns<true>(r[k & 1], nl + 32 * k, c2, 32 * k, lo, hi, acc);
+            add_columns<true>(r, nl + 32 * k, c, 32 * k, lo, hi, acc);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (elect_one()) {
-          mbar_arrive(bar(C_SE + 2 * tile + buf));
-          mbar_arrive(bar(C_LE + qs));
-        }
-        __syncwarp();
+        __syncwarp();  // every lane has read nl
         // a step's columns are added up on their own first: shorter chains of roundings
-        const float2 x = upk2(fadd2(acc[0], acc[1]));
-        total += x.x + x.y;
+        total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
       }
       if (!ok) total = NAN;
+      if (n_steps > 1) {
+        float* hand = handed + n_hand % 3 * CK + t;
+        const uint32_t full = bar(hand_bar + n_hand % 3);
+        if (half == 1) {
+          *hand = total;
+          __syncwarp();
+          if (elect_one()) mbar_arrive(full);
+          __syncwarp();
+        } else {
+          if (!warp_wait(full, n_hand / 3 & 1)) ok = false;
+          total = ok ? total + *hand : NAN;
+        }
+        ++n_hand;
+      }
+      if (!fin) continue;
       if constexpr (SPLIT) {
-        part = total;
+        reinterpret_cast<float*>(smem + SM_X)[3 * CK + t] = total;
       } else if (my.live) {
         store(my, total);
       }
@@ -547,13 +499,11 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   if constexpr (SPLIT) {
     // the cluster's partial sums of the item, added in rank order; every thread of every CTA takes
     // both cluster barriers
-    float* parts = reinterpret_cast<float*>(smem + SM_L);  // (every step has been read)
-    static_assert(NQS * CN >= CK, "one float per key");
-    if (warp >= 4) parts[threadIdx.x - 128] = part;
+    const float* parts = reinterpret_cast<const float*>(smem + SM_X) + 3 * CK;
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     const int share = CK / S, t = rank * share + (int)threadIdx.x;
     if ((int)threadIdx.x < share) {
-      const Item it = make_item(a, Cursor(a, cta, ctas), qpt_log2);
+      const Item it = make_item(a, lens, Cursor(a, cta, ctas), qpt_log2);
       const Mine my = my_key(it, t);
       if (my.live) {
         float total = 0.0f;
@@ -599,10 +549,11 @@ int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream) {
     if (!encode(&mq, a.q, 4, dims, strides, box)) return check_launch(cudaErrorInvalidValue);
   }
   {
-    cuuint64_t dims[2] = {CD, (cuuint64_t)a.num_pages * a.n_kv_heads * 16};
-    cuuint64_t strides[1] = {CD * 2};
-    cuuint32_t box[2] = {64, 16};
-    if (!encode(&mk, a.k_pages, 2, dims, strides, box)) return check_launch(cudaErrorInvalidValue);
+    // pools as (64 dims, 8 rows, 2 halves, 8-row groups): a box is one (page, KV head) block
+    cuuint64_t dims[4] = {64, 8, 2, (cuuint64_t)a.num_pages * a.n_kv_heads * 2};
+    cuuint64_t strides[3] = {CD * 2, 128, 8 * CD * 2};
+    cuuint32_t box[4] = {64, 8, 2, 2};
+    if (!encode(&mk, a.k_pages, 4, dims, strides, box)) return check_launch(cudaErrorInvalidValue);
   }
   const int64_t cap = (int64_t)a.max_blocks * a.page_size;
   const int64_t rows = (int64_t)a.batch * a.n_kv_heads, n_tiles = (cap + CK - 1) / CK;
@@ -613,30 +564,30 @@ int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream) {
   // every CTA a step.
   const int n_queries = a.window > 0 && a.window < a.chunk_len ? a.window : a.chunk_len;
   const int64_t steps = ((int64_t)n_queries * G + CN - 1) / CN;
-  int S = 1;
-  while (S < 8 && 2 * S <= steps && 2 * S * n_tiles * rows <= sms) S *= 2;
-  if (S == 1) {
+  int s_log2 = 0;
+  while (s_log2 < 3 && (2 << s_log2) <= steps && (n_tiles * rows << (s_log2 + 1)) <= sms) ++s_log2;
+  if (s_log2 == 0) {
     static FuncConfigured configured;
     if (!configured.ensure(reinterpret_cast<const void*>(chunk_weights_kernel<false>), C_SMEM)) return PKV_ERR_LAUNCH;
     const int grid = (int)(n_tiles * rows < sms ? n_tiles * rows : sms);
-    chunk_weights_kernel<false><<<grid, CTHREADS, C_SMEM, stream>>>(mq, mk, a, (int)n_tiles, 1);
+    chunk_weights_kernel<false><<<grid, CTHREADS, C_SMEM, stream>>>(mq, mk, a, (int)n_tiles, 0);
     return check_launch(cudaGetLastError());
   }
   static FuncConfigured configured;
   if (!configured.ensure(reinterpret_cast<const void*>(chunk_weights_kernel<true>), C_SMEM)) return PKV_ERR_LAUNCH;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(S * n_tiles * rows), 1, 1);
+  cfg.gridDim = dim3((unsigned)(n_tiles * rows << s_log2), 1, 1);
   cfg.blockDim = dim3(CTHREADS, 1, 1);
   cfg.dynamicSmemBytes = C_SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.x = 1u << s_log2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, chunk_weights_kernel<true>, mq, mk, a, (int)n_tiles, S));
+  return check_launch(cudaLaunchKernelEx(&cfg, chunk_weights_kernel<true>, mq, mk, a, (int)n_tiles, s_log2));
 }
 
 }  // namespace pkv
