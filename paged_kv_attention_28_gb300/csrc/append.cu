@@ -16,11 +16,12 @@
 // bit, and sincospi of its leading bits gives cos and sin. No fp64 arithmetic, whose rate here is
 // a 64th of fp32's.
 //
-// A CTA takes one token. Every thread asks for the rows of its first batch as soon as the token's
-// lengths are in; while they travel, one thread per pair computes the token's cos and sin
-// into shared memory, which the rows of all heads share. Groups of D / 8 lanes take the rows
-// (every query, key and value head), 8 elements a lane in two runs of 4 chosen so that both
-// elements of a pair are in one lane: no exchange but the norm's sum.
+// A CTA takes a few consecutive tokens of a sequence. Groups of D / 8 lanes take a token's rows
+// (every query, key and value head), kRows each at a time, 8 elements a lane in two runs of 4 chosen
+// so that both elements of a pair are in one lane: no exchange but the norm's sum. The next
+// rows, the next token's too, are asked for before the present ones are worked on, and one
+// thread per pair computes the next token's cos and sin into shared memory, which the rows of
+// all heads share.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -31,8 +32,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kRows = 3;  // rows of a lane group in flight
+constexpr int kPage = 16;
 
 // Four consecutive elements of T as one access.
 template <typename T>
@@ -73,38 +74,39 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
   return (u >> 31) ? 0 - v : v;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+template <typename T, int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, int per_cta) {
   using Q4 = Quad<T>;
   using Raw = typename Q4::Raw;
-  constexpr int L = D / 8;              // lanes per row
-  constexpr int GROUPS = kThreads / L;  // rows a CTA works on at a time
-  __shared__ __align__(16) float s_cos[D / 2];
-  __shared__ __align__(16) float s_sin[D / 2];
+  constexpr int L = D / 8;             // lanes per row
+  constexpr int GROUPS = THREADS / L;  // rows a CTA works on at a time
+  __shared__ __align__(16) float s_cos[2][D / 2];
+  __shared__ __align__(16) float s_sin[2][D / 2];
   const int tid = threadIdx.x;
   const int pairs = a.rotary_dim / 2;
-  const int64_t t = blockIdx.x;
-  const int b = (int)(t / a.chunk_len), i = (int)(t % a.chunk_len);
-  const int64_t len = __ldg(a.prefix_lens + b);
-  const int64_t n = a.chunk_lens ? __ldg(a.chunk_lens + b) : a.chunk_len;
+  const int b = blockIdx.y, first = blockIdx.x * per_cta;
+  const int len = __ldg(a.prefix_lens + b);
+  const int n = a.chunk_lens ? __ldg(a.chunk_lens + b) : a.chunk_len;
   const bool bad_n = n < 0 || n > a.chunk_len;
-  if (!bad_n && i >= n) return;  // padding
-  const int64_t at = len + i;
-  const bool bad_len = bad_n || len < 0 || len + n > (int64_t)a.max_blocks * a.page_size;
-  int page = -1;
-  if (!bad_len) page = __ldg(a.block_table + (int64_t)b * a.max_blocks + at / a.page_size);
+  const int end = min(first + per_cta, bad_n ? a.chunk_len : n);  // tokens [first, end)
+  if (first >= end) return;  // padding
+  const bool bad_len = bad_n || len < 0 || (int64_t)len + n > (int64_t)a.max_blocks * kPage;
+  const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
+  const int64_t t0 = (int64_t)b * a.chunk_len;  // the sequence's first token
+  auto page_of = [&](int i) { return bad_len ? -1 : __ldg(table + (len + i) / kPage); };
 
   const int l = tid % L, group = tid / L;
   const int rows = a.n_qo_heads + 2 * a.n_kv_heads;
+  const int batches = (rows + GROUPS * kRows - 1) / (GROUPS * kRows);  // of a token's rows
   // the lane's two runs of four elements, and whether they are rotated
   const bool turned = 8 * l < a.rotary_dim;
   const int o0 = !turned || a.interleaved ? 8 * l : 4 * l;
   const int o1 = !turned || a.interleaved ? 8 * l + 4 : pairs + 4 * l;
-  Raw lo[kRows], hi[kRows];
-  auto load = [&](int base) {
+  auto load = [&](Raw (&lo)[kRows], Raw (&hi)[kRows], int i, int batch) {
+    const int64_t t = t0 + i;
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int r = base + u * GROUPS + group;
+      const int r = (batch * kRows + u) * GROUPS + group;
       lo[u] = Raw{}, hi[u] = Raw{};
       if (r < rows) {
         const bool is_q = r < a.n_qo_heads, is_k = r < a.n_qo_heads + a.n_kv_heads;
@@ -116,102 +118,135 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
       }
     }
   };
-  load(0);
+  Raw next_lo[kRows], next_hi[kRows];
+  load(next_lo, next_hi, first, 0);
+  int next_page = page_of(first);
 
+  uint64_t turn = 0;
+  int axis = -1;  // -1: the pair's outputs are NaN
   if (tid < pairs) {
     const float f = __ldg(a.inv_freq + tid);
-    int axis = a.pair_axis ? __ldg(a.pair_axis + tid) : 0;
+    axis = a.pair_axis ? __ldg(a.pair_axis + tid) : 0;
     if (axis < 0 || axis >= a.n_axes) {
       set_err(a.err_flag, PKV_DEVERR_BAD_AXIS);
       axis = -1;
     }
-    float c = NAN, s = NAN;
-    if (axis >= 0 && fabsf(f) < INFINITY) {
-      const int64_t pos = a.positions ? __ldg(a.positions + axis * ((int64_t)a.batch * a.chunk_len) + t) : at;
-      const int64_t phase = (int64_t)((uint64_t)pos * turn_fraction(f));  // 2^64 to a turn
-      sincospif((float)phase * 1.0842021724855044e-19f, &s, &c);          // 2^-63: half turns
+    if (!(fabsf(f) < INFINITY)) axis = -1;
+    turn = turn_fraction(f);
+  }
+  auto angles = [&](int i) {
+    if (tid < pairs) {
+      float c = NAN, s = NAN;
+      if (axis >= 0) {
+        const int64_t pos =
+            a.positions ? __ldg(a.positions + axis * ((int64_t)a.batch * a.chunk_len) + t0 + i) : (int64_t)len + i;
+        const int64_t phase = (int64_t)((uint64_t)pos * turn);  // 2^64 to a turn
+        sincospif((float)phase * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
+      }
+      s_cos[i & 1][tid] = c;
+      s_sin[i & 1][tid] = s;
     }
-    s_cos[tid] = c;
-    s_sin[tid] = s;
-  }
-  if (page < 0 || page >= a.num_pages) {
-    page = -1;
-    if (tid == 0) set_err(a.err_flag, bad_len ? PKV_DEVERR_BAD_LEN : PKV_DEVERR_BAD_PAGE);
-  }
-  const int64_t slot = ((int64_t)page * a.n_kv_heads) * a.page_size + at % a.page_size;  // of KV head 0
+  };
+  angles(first);
   __syncthreads();
 
-  for (int base = 0;;) {
+  for (int i = first; i < end; ++i) {
+    int page = next_page;
+    if (page < 0 || page >= a.num_pages) {
+      page = -1;
+      if (tid == 0) set_err(a.err_flag, bad_len ? PKV_DEVERR_BAD_LEN : PKV_DEVERR_BAD_PAGE);
+    }
+    const int64_t slot = (int64_t)page * a.n_kv_heads * kPage + (len + i) % kPage;  // of KV head 0
+    for (int batch = 0; batch < batches; ++batch) {
+      Raw lo[kRows], hi[kRows];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int r = base + u * GROUPS + group;
-      const bool is_q = r < a.n_qo_heads, is_k = r < a.n_qo_heads + a.n_kv_heads;
-      float v[8];
-      Q4::get(lo[u], v, 0);
-      Q4::get(hi[u], v, 4);
-      float ss = 0.0f;
+      for (int u = 0; u < kRows; ++u) lo[u] = next_lo[u], hi[u] = next_hi[u];
+      if (batch + 1 < batches) {
+        load(next_lo, next_hi, i, batch + 1);
+      } else if (i + 1 < end) {
+        load(next_lo, next_hi, i + 1, 0);
+        next_page = page_of(i + 1);
+        angles(i + 1);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+      for (int u = 0; u < kRows; ++u) {
+        const int r = (batch * kRows + u) * GROUPS + group;
+        const bool is_q = r < a.n_qo_heads, is_k = r < a.n_qo_heads + a.n_kv_heads;
+        float v[8];
+        Q4::get(lo[u], v, 0);
+        Q4::get(hi[u], v, 4);
+        float ss = 0.0f;
 #pragma unroll
-      for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      if (r >= rows) continue;
-      if (is_k) {  // (queries too)
-        const T* w = static_cast<const T*>(is_q ? a.q_norm : a.k_norm);
-        if (w) {
-          const float s = rsqrtf(ss * (1.0f / D) + a.eps);
-          float wv[8];
-          Q4::get(*reinterpret_cast<const Raw*>(w + o0), wv, 0);
-          Q4::get(*reinterpret_cast<const Raw*>(w + o1), wv, 4);
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = v[e] * s * wv[e];
-        }
-        if (turned) {
-          const float4 c4 = *reinterpret_cast<const float4*>(s_cos + 4 * l);
-          const float4 s4 = *reinterpret_cast<const float4*>(s_sin + 4 * l);
-          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-          if (a.interleaved) {
+        for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        if (r >= rows) continue;
+        if (is_k) {  // (queries too)
+          const T* w = static_cast<const T*>(is_q ? a.q_norm : a.k_norm);
+          if (w) {
+            const float s = rsqrtf(ss * (1.0f / D) + a.eps);
+            float wv[8];
+            Q4::get(*reinterpret_cast<const Raw*>(w + o0), wv, 0);
+            Q4::get(*reinterpret_cast<const Raw*>(w + o1), wv, 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float xa = v[2 * j], xb = v[2 * j + 1];
-              v[2 * j] = xa * c[j] - xb * s[j];
-              v[2 * j + 1] = xb * c[j] + xa * s[j];
-            }
-          } else {
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * s * wv[e];
+          }
+          if (turned) {
+            const float4 c4 = *reinterpret_cast<const float4*>(s_cos[i & 1] + 4 * l);
+            const float4 s4 = *reinterpret_cast<const float4*>(s_sin[i & 1] + 4 * l);
+            const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+            if (a.interleaved) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float xa = v[j], xb = v[j + 4];
-              v[j] = xa * c[j] - xb * s[j];
-              v[j + 4] = xb * c[j] + xa * s[j];
+              for (int j = 0; j < 4; ++j) {
+                const float xa = v[2 * j], xb = v[2 * j + 1];
+                v[2 * j] = xa * c[j] - xb * s[j];
+                v[2 * j + 1] = xb * c[j] + xa * s[j];
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float xa = v[j], xb = v[j + 4];
+                v[j] = xa * c[j] - xb * s[j];
+                v[j + 4] = xb * c[j] + xa * s[j];
+              }
             }
           }
-        }
-        if (is_q && page < 0) {
+          if (is_q && page < 0) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = NAN;
+            for (int e = 0; e < 8; ++e) v[e] = NAN;
+          }
+          lo[u] = Q4::put(v, 0);
+          hi[u] = Q4::put(v, 4);
         }
-        lo[u] = Q4::put(v, 0);
-        hi[u] = Q4::put(v, 4);
+        T* dst;
+        if (is_q) {
+          dst = static_cast<T*>(a.q_out) + ((t0 + i) * a.n_qo_heads + r) * D;
+        } else {
+          if (page < 0) continue;
+          const int h = r - a.n_qo_heads - (is_k ? 0 : a.n_kv_heads);
+          dst = static_cast<T*>(is_k ? a.k_pages : a.v_pages) + (slot + h * kPage) * D;
+        }
+        *reinterpret_cast<Raw*>(dst + o0) = lo[u];
+        *reinterpret_cast<Raw*>(dst + o1) = hi[u];
       }
-      T* dst;
-      if (is_q) {
-        dst = static_cast<T*>(a.q_out) + (t * a.n_qo_heads + r) * D;
-      } else {
-        if (page < 0) continue;
-        const int h = r - a.n_qo_heads - (is_k ? 0 : a.n_kv_heads);
-        dst = static_cast<T*>(is_k ? a.k_pages : a.v_pages) + (slot + (int64_t)h * a.page_size) * D;
-      }
-      *reinterpret_cast<Raw*>(dst + o0) = lo[u];
-      *reinterpret_cast<Raw*>(dst + o1) = hi[u];
     }
-    base += GROUPS * kRows;
-    if (base >= rows) break;
-    load(base);
+    __syncthreads();  // the next token's angles are in, and this one's may be overwritten
   }
 }
 
 template <typename T, int D>
 int launch_t(const AppendArgs& a, cudaStream_t stream) {
-  append_kernel<T, D><<<(unsigned)((int64_t)a.batch * a.chunk_len), kThreads, 0, stream>>>(a);
+  int sms = device_sm_count();
+  if (sms <= 0) sms = 148;
+  // Few tokens: one per CTA of 256 threads, which puts most rows at work at once. Many: two per CTA
+  // of 128 threads (one or four are 3 to 8 % slower, 256 or 64 threads 10 and 30 %).
+  if ((int64_t)a.batch * a.chunk_len <= 16 * (int64_t)sms) {
+    append_kernel<T, D, 256><<<dim3((unsigned)a.chunk_len, (unsigned)a.batch), 256, 0, stream>>>(a, 1);
+  } else {
+    constexpr int kPer = 2;
+    append_kernel<T, D, 128>
+        <<<dim3((unsigned)((a.chunk_len + kPer - 1) / kPer), (unsigned)a.batch), 128, 0, stream>>>(a, kPer);
+  }
   return check_launch(cudaGetLastError());
 }
 

@@ -577,7 +577,7 @@ int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_
   if (!aligned16(k_pages) || !aligned16(v_pages)) return PKV_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || page_size != 16 || rotary_dim % 8 || n_axes > 4)
     return PKV_ERR_UNSUPPORTED;
-  if ((int64_t)batch * chunk_len > 0x7fffffffL || n_qo_heads > (1 << 20) || n_kv_heads > (1 << 20))
+  if (batch > 65535 || n_qo_heads > (1 << 20) || n_kv_heads > (1 << 20))
     return PKV_ERR_UNSUPPORTED;
   AppendArgs a{q, k, v, q_stride, k_stride, v_stride, q_norm, k_norm, norm_eps, inv_freq, rotary_dim,
                interleaved, positions, n_axes, pair_axis, block_table, prefix_lens, chunk_lens, q_out,

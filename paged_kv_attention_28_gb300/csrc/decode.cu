@@ -97,6 +97,7 @@ bool decode_supported(int dtype, int head_dim, int page_size, int group) {
 
 int launch_decode_partials(const DecodeArgs& a, cudaStream_t stream) {
   if (decode_tc_supported(a)) return launch_decode_tc(a, stream);
+  if (a.logits) return dispatch_decode_logits(a, stream);
   return a.unified ? dispatch_decode_unified(a, stream) : dispatch_decode<false>(a, stream);
 }
 
@@ -104,7 +105,6 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   const int rc = decode_tc_supported(a) ? launch_decode_tc(a, stream)
                  : a.fp8                  ? dispatch_decode_fp8(a, stream)
                  : a.unified              ? dispatch_decode_unified(a, stream)
-                 : a.logits               ? dispatch_decode_logits(a, stream)
                                           : dispatch_decode<false>(a, stream);
   if (rc != PKV_OK) return rc;
   if (a.num_splits > 1) return launch_merge_splits(a, stream);

@@ -1,14 +1,16 @@
 // Linear layer with its epilogue: y[m][n] = act(x[m][k] w[n][k]^T + bias[n]) + residual[m][n].
 //
 // Up to 64 tokens the weights stream through the tensor cores as in the flat GEMM (flat_gemm.cu
-// with its epilogue instantiation). Above, this file's tiled kernel: a persistent CTA per SM
-// multiplies 128 tokens x BN features with tcgen05, fp32 accumulators in tensor memory,
-// operands by TMA through a ring of 64-column stages. The accumulator is double-buffered, so the
-// four epilogue warps read one tile out of tensor memory, apply bias, activation and residual in
-// fp32 and store it (one rounding) while the next tile's products run.
+// with its epilogue instantiation). Above, this file's kernel: persistent pairs of CTAs, a tile of
+// 256 tokens x BN features per pair. One tcgen05 product spans both SMs of the pair: each holds its
+// 128 tokens and half of the features, so that a CTA reads half the weights a single one would, and
+// the fp32 accumulators of its tokens. Operands come by TMA through a ring of six 64-column blocks;
+// the accumulator is double-buffered, so four epilogue warps read one tile out of tensor memory,
+// apply bias, activation and residual in fp32 and store it (one rounding) while the next tile's
+// products run.
 //
-// BN is 256 where that still gives every SM a tile, else 128 or 64: a small problem needs
-// more tiles than wide ones give, a large one wants the operand reuse of the widest.
+// Bound: the tensor cores, 2 m n k operations; for few tokens the weights' bytes. BN is the multiple
+// of 32 for which the rounds of tiles over the pairs take least (choose_width).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -25,29 +27,17 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // prefill.cu
 
 namespace {
 
-constexpr int LBM = 128, LBK = 64;
-constexpr int ASTG = LBM * LBK * 2;
+constexpr int LBK = 64;              // K per block of a stage: one 128-byte swizzled row
+constexpr int BLK = 128 * LBK * 2;   // a CTA's tokens (or most features) of a block
 constexpr int LTHREADS = 256;
 constexpr int PANEL = 16;  // token tiles walked before the next feature tile: their x stays in L2
-
-template <int BN>
-struct LinCfg {
-  static constexpr int BSTG = BN * LBK * 2;
-  static constexpr int NST = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr int SM_A = 0, SM_B = NST * ASTG, SM_BAR = SM_B + NST * BSTG;
-  // barriers: full[NST], empty[NST], acc_full[2], acc_empty[2], drain
-  static constexpr int NBAR = 2 * NST + 5;
-  static constexpr int SM_MISC = SM_BAR + NBAR * 8, SMEM = SM_MISC + 16 + 1024;
-  static constexpr int TMEM = 2 * BN;
-  static_assert(SMEM <= 232448, "shared memory per CTA");
-};
 
 struct LinArgs {
   __nv_bfloat16* y;
   Epilogue ep;
-  int m, n, n_kc;
+  int m, n, n_kc;  // n_kc: stages of K
   int tiles_m, tiles;
-  bool vec;  // rows of y and of the residual are 16-byte aligned
+  int vec;  // bytes to which the rows of y and of the residual are aligned: 32, 16, or 0 for neither
   int32_t* err_flag;
 };
 
@@ -65,14 +55,15 @@ __device__ __forceinline__ void tile_at(int i, int tiles_m, int tiles_n, int& tm
   tn = r / rows;
 }
 
-// 32 consecutive features of one token.
-__device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[32], int row, int col) {
+// N consecutive features of one token, those from `end` on not stored.
+template <int N>
+__device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[N], int row, int col, int end) {
   const __nv_bfloat16* bias = a.ep.bias;
   const int64_t at = (int64_t)row * a.n + col;
-  if (a.vec && col + 32 <= a.n) {
+  if (a.vec && col + N <= end) {
     if (bias) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < N; i += 2) {
         const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(bias + col + i));
         v[i] += b.x, v[i + 1] += b.y;
       }
@@ -80,7 +71,7 @@ __device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[32], int
     activate_all(v, a.ep.activation);
     if (a.ep.residual) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
+      for (int i = 0; i < N; i += 8) {
         const uint4 r = *reinterpret_cast<const uint4*>(a.ep.residual + at + i);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -90,20 +81,31 @@ __device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[32], int
         }
       }
     }
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      *reinterpret_cast<uint4*>(a.y + at + i) = make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
-                                                           pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
+    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    if (a.vec == 32) {  // whole 32-byte sectors (half-sector stores cost 4 % of a large product)
+#pragma unroll
+      for (int i = 0; i < N / 2; i += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a.y + at + 2 * i), "r"(w[i]),
+                     "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                     "r"(w[i + 7])
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; i += 4)
+        *reinterpret_cast<uint4*>(a.y + at + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
   } else {
     if (bias) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i < a.n) v[i] += __bfloat162float(bias[col + i]);
+      for (int i = 0; i < N; ++i)
+        if (col + i < end) v[i] += __bfloat162float(bias[col + i]);
     }
     activate_all(v, a.ep.activation);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (col + i < a.n) {
+    for (int i = 0; i < N; ++i) {
+      if (col + i < end) {
         const float r = a.ep.residual ? __bfloat162float(a.ep.residual[at + i]) : 0.0f;
         a.y[at + i] = __float2bfloat16_rn(a.ep.residual ? v[i] + r : v[i]);
       }
@@ -111,40 +113,101 @@ __device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[32], int
   }
 }
 
-template <int BN>
+constexpr int PBM = 256;  // tokens of a pair's tile, 128 per CTA
+
+// SUB: 64-column blocks per stage. One for wide tiles, whose stage is bound by its products; two
+// for narrow ones, where the barriers of a stage weigh more (256 x 4096 x 4096: 22.9 to 16.6 us).
+template <int SUB>
+struct LinCfg {
+  static constexpr int PST = 6 / SUB, STG = SUB * BLK;  // stages; bytes of one operand's stage
+  static constexpr int SM_B = PST * STG, SM_BAR = 2 * PST * STG, NBAR = 2 * PST + 5, SM_MISC = SM_BAR + NBAR * 8,
+                       SMEM = SM_MISC + 16 + 1024;
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+__device__ __forceinline__ uint32_t pair_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address of the same shared-memory location in the pair's first CTA.
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A load into this CTA's shared memory that counts on a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(mbar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar),
+      "h"((unsigned short)3)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
+}
+
+// A cluster of two CTAs per tile of 256 tokens x bn features. The first CTA's MMA warp issues the
+// products of both; loads of both count on its `full` barriers, its commits free the stages of
+// both, and the epilogue warps of both hand the accumulators back to it.
+template <int SUB>
 __global__ void __launch_bounds__(LTHREADS, 1)
-linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const LinArgs a) {
-  using C = LinCfg<BN>;
+linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw, const LinArgs a,
+                   int bn) {
+  using C = LinCfg<SUB>;
+  constexpr int PST = C::PST;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
   unsigned char* smem = smem_raw + pad;
   const uint32_t sb = raw + pad;
   LMisc* misc = reinterpret_cast<LMisc*>(smem + C::SM_MISC);
-  const uint32_t full = sb + C::SM_BAR, empty = full + 8 * C::NST, acc_full = empty + 8 * C::NST,
-                 acc_empty = acc_full + 16, drain = acc_empty + 16;
+  const uint32_t full = sb + C::SM_BAR, empty = full + 8 * PST, acc_full = empty + 8 * PST, acc_empty = acc_full + 16,
+                 drain = acc_empty + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)pair_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles_n = a.tiles / a.tiles_m;
+  const int half = bn / 2;  // features per CTA
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::NST; ++s) {
+    for (int s = 0; s < PST; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full + 8 * s, 1);
-      mbar_init(acc_empty + 8 * s, 4);
+      mbar_init(acc_empty + 8 * s, 8);
     }
     mbar_init(drain, 1);
     misc->abort_ = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(smem_u32(&misc->tmem_base), C::TMEM);
-    tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&misc->tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // both CTAs' barriers exist before either signals the other's
   tc_fence_after();
   const uint32_t tmem = misc->tmem_base;
   volatile int* aborted = &misc->abort_;
@@ -156,7 +219,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
   };
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ TMA producer, one in each CTA
     if (elect_one()) {
       tma_prefetch_desc(&mx);
       tma_prefetch_desc(&mw);
@@ -164,59 +227,71 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     __syncwarp();
     uint32_t c = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < a.tiles; i += gridDim.x) {
+    for (int i = pair; ok && i < a.tiles; i += pairs) {
       int tm, tn;
       tile_at(i, a.tiles_m, tiles_n, tm, tn);
-      for (int kc = 0; kc < a.n_kc; ++kc, ++c) {
-        const uint32_t s = c % C::NST;
-        if (c >= C::NST && !warp_wait(empty + 8 * s, (c / C::NST - 1) & 1)) ok = false;
-        if (__any_sync(0xffffffffu, *aborted)) ok = false;
+      if (__any_sync(0xffffffffu, *aborted)) ok = false;  // (asked once a tile: the producers' loop is the critical path)
+      for (int kc = 0; ok && kc < a.n_kc; ++kc, ++c) {
+        const uint32_t s = c % PST;
+        if (c >= PST && !warp_wait(empty + 8 * s, (c / PST - 1) & 1)) ok = false;
         if (!ok) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(full + 8 * s, ASTG + C::BSTG);
-          tma_load_2d(sb + C::SM_A + s * ASTG, &mx, kc * LBK, tm * LBM, full + 8 * s);
-          tma_load_2d(sb + C::SM_B + s * C::BSTG, &mw, kc * LBK, tn * BN, full + 8 * s);
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * SUB * (BLK + half * LBK * 2));
+          const uint32_t bar = in_first(full + 8 * s);
+#pragma unroll
+          for (int h = 0; h < SUB; ++h) {
+            const int k0 = (kc * SUB + h) * LBK;  // (columns past k read as 0)
+            tma_load_2d_pair(sb + s * C::STG + h * BLK, &mx, k0, tm * PBM + rank * 128, bar);
+            tma_load_2d_pair(sb + C::SM_B + s * C::STG + h * BLK, &mw, k0, tn * bn + rank * half, bar);
+          }
         }
         __syncwarp();
       }
     }
     if (!ok) give_up();
-    bool drained = true;  // every issued copy lands before the shared memory is released
-    for (uint32_t s = 0; s < (uint32_t)C::NST && s < c; ++s)
-      drained &= warp_wait(full + 8 * s, ((c - 1 - s) / C::NST) & 1);
-    if (!drained) give_up();
-  } else if (warp == 1) {
+    // the last signals that free this CTA's stages have come before it may end
+    for (uint32_t s = 0; ok && s < (uint32_t)PST && s < c; ++s) ok = warp_wait(empty + 8 * s, ((c - 1 - s) / PST) & 1);
+    if (!ok) give_up();
+    if (rank == 0) {  // every copy, the other CTA's too, lands before the shared memory is released
+      bool drained = true;
+      for (uint32_t s = 0; s < (uint32_t)PST && s < c; ++s)
+        drained &= warp_wait(full + 8 * s, ((c - 1 - s) / PST) & 1);
+      if (!drained) give_up();
+    }
+  } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t idesc = idesc_bf16_f32(LBM, BN, false, false);
-    const uint64_t da0 = smem_desc(sb + C::SM_A, 16, 1024, kSwizzle128B);
+    const uint32_t idesc = idesc_bf16_f32(PBM, bn, false, false);
+    const uint64_t da0 = smem_desc(sb, 16, 1024, kSwizzle128B);
     const uint64_t db0 = smem_desc(sb + C::SM_B, 16, 1024, kSwizzle128B);
     uint32_t c = 0, t = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < a.tiles; i += gridDim.x, ++t) {
+    for (int i = pair; ok && i < a.tiles; i += pairs, ++t) {
       const uint32_t buf = t & 1;
       if (t >= 2 && !warp_wait(acc_empty + 8 * buf, (t / 2 - 1) & 1)) ok = false;
       tc_fence_after();
       for (int kc = 0; ok && kc < a.n_kc; ++kc, ++c) {
-        const uint32_t s = c % C::NST;
-        if (!warp_wait(full + 8 * s, (c / C::NST) & 1)) {
+        const uint32_t s = c % PST;
+        if (!warp_wait(full + 8 * s, (c / PST) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t da = da0 + (uint64_t)((s * ASTG) >> 4), db = db0 + (uint64_t)((s * C::BSTG) >> 4);
+          const uint64_t da = da0 + (uint64_t)((s * C::STG) >> 4), db = db0 + (uint64_t)((s * C::STG) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < LBK / 16; ++kk)
-            mma_bf16_ss(tmem + buf * BN, da + (uint64_t)(kk * 2), db + (uint64_t)(kk * 2), idesc,
-                        (kc > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(empty + 8 * s);
-          if (kc == a.n_kc - 1) mma_commit(acc_full + 8 * buf);
+          for (int kk = 0; kk < SUB * LBK / 16; ++kk) {
+            const uint64_t off = (uint64_t)((kk / 4 * BLK + kk % 4 * 32) >> 4);
+            mma_pair(tmem + buf * 256, da + off, db + off, idesc, (kc > 0 || kk > 0) ? 1u : 0u);
+          }
+          commit_pair(empty + 8 * s);
+          if (kc == a.n_kc - 1) commit_pair(acc_full + 8 * buf);
         }
         __syncwarp();
       }
     }
     if (!ok) give_up();
-    if (elect_one()) mma_commit(drain);  // every issued product finishes before TMEM is freed
+    if (elect_one())  // every issued product finishes before TMEM is freed
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain) : "memory");
     __syncwarp();
     if (!warp_wait(drain, 0)) give_up();
   } else if (warp >= 4) {
@@ -224,16 +299,17 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     const int wq = warp & 3;
     uint32_t t = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < a.tiles; i += gridDim.x, ++t) {
+    for (int i = pair; i < a.tiles; i += pairs, ++t) {
       int tm, tn;
       tile_at(i, a.tiles_m, tiles_n, tm, tn);
       const uint32_t buf = t & 1;
       if (ok && !warp_wait(acc_full + 8 * buf, (t / 2) & 1)) ok = false;
       tc_fence_after();
-      const int row = tm * LBM + wq * 32 + lane;
-      const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + buf * BN;
+      const int row = tm * PBM + rank * 128 + wq * 32 + lane;
+      const int end = min(a.n, (tn + 1) * bn);
+      const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + buf * 256;
 #pragma unroll 1
-      for (int cc = 0; cc < BN; cc += 32) {
+      for (int cc = 0; cc + 32 <= bn; cc += 32) {
         uint32_t r[32];
         if (ok) {
           tmem_ld32(src + cc, r);
@@ -242,22 +318,22 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
         float v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = ok ? __uint_as_float(r[k]) : NAN;
-        const int col = tn * BN + cc;
-        if (row < a.m && col < a.n) finish_row(a, v, row, col);
+        if (row < a.m && tn * bn + cc < end) finish_row(a, v, row, tn * bn + cc, end);
         __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
-      if (ok && elect_one()) mbar_arrive(acc_empty + 8 * buf);
+      if (ok && elect_one()) arrive_remote(in_first(acc_empty + 8 * buf));
       __syncwarp();
     }
     if (!ok) give_up();
   }
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // neither CTA's memory goes while the other's products or signals may touch it
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
@@ -273,39 +349,73 @@ bool encode_rows(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
-int launch_tiled(const LinearArgs& p, int sms, cudaStream_t stream) {
-  using C = LinCfg<BN>;
-  CUtensorMap mx, mw;
-  if (!encode_rows(&mx, p.x, (uint64_t)p.k, (uint64_t)p.m, LBM) ||
-      !encode_rows(&mw, p.w, (uint64_t)p.k, (uint64_t)p.n, BN))
-    return check_launch(cudaErrorInvalidValue);
-  static FuncConfigured configured;
-  if (!configured.ensure(reinterpret_cast<const void*>(linear_kernel<BN>), C::SMEM)) return PKV_ERR_LAUNCH;
-  const int64_t tm = ((int64_t)p.m + LBM - 1) / LBM, tn = ((int64_t)p.n + BN - 1) / BN;
-  if (tm * tn > 0x7fffffffL) return PKV_ERR_UNSUPPORTED;
-  const uintptr_t odd = reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.residual);
-  const uintptr_t odd_bias = reinterpret_cast<uintptr_t>(p.bias) & 3;
-  LinArgs a{static_cast<__nv_bfloat16*>(p.y),
-            Epilogue{static_cast<const __nv_bfloat16*>(p.bias), static_cast<const __nv_bfloat16*>(p.residual), p.activation},
-            p.m, p.n, (p.k + LBK - 1) / LBK, (int)tm, (int)(tm * tn), p.n % 8 == 0 && (odd & 15) == 0 && odd_bias == 0,
-            p.err_flag};
-  const unsigned grid = (unsigned)(tm * tn < sms ? tm * tn : sms);
-  linear_kernel<BN><<<grid, LTHREADS, C::SMEM, stream>>>(mx, mw, a);
-  return check_launch(cudaGetLastError());
+// The feature width for which the tiles take least. Measured for k = 4096: a round of tiles of
+// width 256, 224, 192, 160, 128, 96, 64, 32 takes 20.4, 18.1, 16.0, 14.8, 13.3, 12.2, 11.4, 10.7 us, the
+// wide ones their products, the narrow ones the loads and barriers of a stage; the costs below are
+// those in 10 ns. What does not fill a round of the pairs is lost. A product over a pair takes
+// multiples of 32 from 32 to 256.
+int choose_width(int64_t tiles_m, int n, int pairs) {
+  int best_w = 256;
+  int64_t best = -1;
+  for (int w = 256; w >= 32; w -= 32) {
+    const int64_t tiles = tiles_m * (((int64_t)n + w - 1) / w);
+    const int64_t round = 7 * w + 250 > 3 * w + 1000 ? 7 * w + 250 : 3 * w + 1000;
+    const int64_t cost = (tiles + pairs - 1) / pairs * round;
+    if (best < 0 || cost < best) {
+      best = cost;
+      best_w = w;
+    }
+  }
+  return best_w;
 }
+
+template <int SUB>
+int launch_t(const CUtensorMap& mx, const CUtensorMap& mw, const LinArgs& a, int bn, unsigned grid, cudaStream_t stream) {
+  static FuncConfigured configured;
+  if (!configured.ensure(reinterpret_cast<const void*>(linear_kernel<SUB>), LinCfg<SUB>::SMEM)) return PKV_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(LTHREADS, 1, 1);
+  cfg.dynamicSmemBytes = LinCfg<SUB>::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return check_launch(cudaLaunchKernelEx(&cfg, linear_kernel<SUB>, mx, mw, a, bn));
+}
+
+constexpr int kWide = 224;  // tiles from this width take one block per stage
 
 }  // namespace
 
-int launch_linear(const LinearArgs& a, cudaStream_t stream) {
-  if (a.m <= kFlatGemmMaxM) return launch_flat_linear(a, stream);
+int launch_linear(const LinearArgs& p, cudaStream_t stream) {
+  if (p.m <= kFlatGemmMaxM) return launch_flat_linear(p, stream);
+  if (p.m > 0x7fffff00 || p.n > 0x7fffff00) return PKV_ERR_UNSUPPORTED;  // (tile ends fit 32 bits)
   int sms = device_sm_count();
-  if (sms <= 0) sms = 148;
-  const int64_t tm = ((int64_t)a.m + LBM - 1) / LBM;
-  auto tiles = [&](int bn) { return tm * (((int64_t)a.n + bn - 1) / bn); };
-  if (tiles(256) >= sms) return launch_tiled<256>(a, sms, stream);
-  if (tiles(128) >= sms) return launch_tiled<128>(a, sms, stream);
-  return launch_tiled<64>(a, sms, stream);
+  if (sms <= 1) sms = 148;
+  const int pairs = sms / 2;
+  const int64_t tm = ((int64_t)p.m + PBM - 1) / PBM;
+  const int bn = choose_width(tm, p.n, pairs);
+  const int64_t tiles = tm * (((int64_t)p.n + bn - 1) / bn);
+  if (tiles > 0x7fffffffL) return PKV_ERR_UNSUPPORTED;
+  const uintptr_t rows = reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.residual);
+  const bool bias_pairs = (reinterpret_cast<uintptr_t>(p.bias) & 3) == 0;
+  const int vec = !bias_pairs ? 0 : p.n % 16 == 0 && rows % 32 == 0 ? 32 : p.n % 8 == 0 && rows % 16 == 0 ? 16 : 0;
+  const int block = bn >= kWide ? LBK : 2 * LBK;
+  const LinArgs a{static_cast<__nv_bfloat16*>(p.y),
+                  Epilogue{static_cast<const __nv_bfloat16*>(p.bias), static_cast<const __nv_bfloat16*>(p.residual),
+                           p.activation},
+                  p.m, p.n, (p.k + block - 1) / block, (int)tm, (int)tiles, vec, p.err_flag};
+  const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
+  CUtensorMap mx, mw;
+  if (!encode_rows(&mx, p.x, (uint64_t)p.k, (uint64_t)p.m, 128) ||
+      !encode_rows(&mw, p.w, (uint64_t)p.k, (uint64_t)p.n, (uint32_t)bn / 2))
+    return check_launch(cudaErrorInvalidValue);
+  return bn >= kWide ? launch_t<1>(mx, mw, a, bn, grid, stream) : launch_t<2>(mx, mw, a, bn, grid, stream);
 }
 
 }  // namespace pkv

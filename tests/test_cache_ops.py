@@ -92,7 +92,7 @@ def append_args(b, **kw):
     (dict(kp=ODD), -1), (dict(vp=ctypes.c_void_p((1 << 20) + 8)), -1), (dict(qn=P, eps=float("nan")), -1),
     (dict(qn=P, eps=-1.0), -1), (dict(qn=ODD), -1), (dict(qs=1024, out=P), -1), (dict(mb=1 << 28), -1),
     (dict(d=96, qs=8 * 96, ks=192, vs=192), -2), (dict(page=32), -2), (dict(rot=12), -2), (dict(axes=5), -2),
-    (dict(batch=1 << 20, chunk=1 << 20), -2), (dict(batch=0), 0), (dict(chunk=0, q=None), 0),
+    (dict(batch=1 << 17), -2), (dict(batch=0), 0), (dict(chunk=0, q=None), 0),
 ])
 def test_append_refuses(b, bad, want):
     assert b.lib.attn_qk_norm_rope_append(*append_args(b, **bad)) == want
