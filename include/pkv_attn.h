@@ -93,6 +93,7 @@ extern "C" {
  *   accumulated weights, eviction : as decode (eviction: any head count); over a chunk as the
  *                      chunked prefill: PKV_BF16, head_dim 128, page_size 16, groups dividing 128
  *   linear           : PKV_BF16; any m and n; k a multiple of 8
+ *   accumulated weights over a chunk, eviction : up to 2^30 tokens per sequence
  */
 
 /* Human-readable name of a status code. Static storage; never NULL. */
@@ -521,7 +522,7 @@ int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_
  *   new_lens        : int32 [batch], out: min(n, budget)
  *   new_sums        : fp32 [batch][n_kv_heads][new_max_blocks * page_size], out: the kept
  *                     tokens' sums, 0 at and past the new length
- * Outputs must not overlap inputs. A length < 0 or past the table sets PKV_DEVERR_BAD_LEN and
+ * Outputs must not overlap inputs (the same address is refused). A length < 0 or past the table sets PKV_DEVERR_BAD_LEN and
  * counts as 0. A bad entry of block_table sets PKV_DEVERR_BAD_PAGE and makes the rows NaN; a bad
  * entry of new_block_table sets it too and its rows are not copied.
  */
@@ -552,8 +553,8 @@ int attn_linear(const void* x, const void* w, const void* bias, const void* resi
  * Failure-handling hook for tests (the pages have no counterpart). It lets a test make a
  * bounded wait inside the decode kernel run out, without faulting or hanging anything:
  * after attn_debug_decode_stall(page, wait_limit_ns) with page >= 0, every launch of
- * attn_decode_paged, attn_decode_paged_unified_max, attn_decode_paged_fp8 and
- * attn_decode_paged_noalloc in this process has the producer warp of each CTA withhold
+ * attn_decode_paged, attn_decode_paged_unified_max, attn_decode_paged_weights,
+ * attn_decode_paged_fp8 and attn_decode_paged_noalloc in this process has the producer warp of each CTA withhold
  * the copies of the page-th page of its split (on the tensor-core path: the K copies of
  * the 128-key tile that holds it) and the arrival that would announce them, and every
  * pipeline wait of those launches gives up after wait_limit_ns nanoseconds (0 keeps the

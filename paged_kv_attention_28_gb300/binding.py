@@ -143,12 +143,18 @@ def _ptr(t):
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _stream(stream=None, device=None):
+    """The handle of ``stream``, or of the current one (of ``device``, the current device)."""
     if stream is not None:
         return stream.cuda_stream
     if _current_raw_stream is not None:
-        return _current_raw_stream(torch.cuda.current_device())
+        return _current_raw_stream(torch.cuda.current_device() if device is None else device)
     return torch.cuda.current_stream().cuda_stream
+
+
+def _device_of(t: torch.Tensor) -> int:
+    """The current device, where every tensor of a call has to be (-2 for a host tensor: no device)."""
+    return torch.cuda.current_device() if t.is_cuda else -2
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
@@ -421,7 +427,7 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chu
     if D2 != D:
         raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
     max_blocks = block_table.shape[1]
-    dev, dtype, need = torch.cuda.current_device() if q.is_cuda else -2, q.dtype, _fast_need
+    dev, dtype, need = _device_of(q), q.dtype, _fast_need
     qs = _token_rows(q, "q", dev, dtype, rows)
     ks = _token_rows(k, "k", dev, dtype, (B, C, Hkv, D))
     vs = _token_rows(v, "v", dev, dtype, (B, C, Hkv, D))
@@ -441,7 +447,7 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chu
     st = _pycall.attn_qk_norm_rope_append(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
         None if q_norm is None else need(q_norm, "q_norm", dev, dtype, (D,)),
-        None if k_norm is None else need(k_norm, "k_norm", dev, dtype, (D,)), eps, inv_freq, rot,
+        None if k_norm is None else need(k_norm, "k_norm", dev, dtype, (D,)), float(eps), inv_freq, rot,
         1 if interleaved else 0, positions, n_axes,
         None if pair_axis is None else need(pair_axis, "pair_axis", dev, torch.int32, (rot // 2,)),
         need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
@@ -449,7 +455,7 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chu
         None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, torch.int32, (B,)),
         need(out, "out", dev, dtype, rows), need(k_pages, "k_pages", dev, dtype, None),
         need(v_pages, "v_pages", dev, dtype, k_pages.shape), B, C, max_blocks, num_pages, Hq, Hkv, D, P, _dt(q),
-        _ptr(err_flag), _stream(stream))
+        _ptr(err_flag), _stream(stream, dev))
     _check(st, "attn_qk_norm_rope_append")
     return out
 
@@ -475,7 +481,7 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums,
     if D2 != D:
         raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
     max_blocks = block_table.shape[1]
-    dev, dtype, need = torch.cuda.current_device() if q.is_cuda else -2, q.dtype, _fast_need
+    dev, dtype, need = _device_of(q), q.dtype, _fast_need
     q_ptr = need(q, "q", dev, None, None)
     sums = (B, Hkv, max_blocks * P)
     in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, torch.float32, sums)
@@ -495,9 +501,9 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums,
         q_ptr, need(k_pages, "k_pages", dev, dtype, None), need(v_pages, "v_pages", dev, dtype, k_pages.shape),
         need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
         need(kv_lens, "kv_lens", dev, torch.int32, (B,)), need(out, "out", dev, dtype, (B, Hq, D)),
-        need(lse, "lse", dev, torch.float32, (B, Hq)), in_ptr, out_ptr, B, max_blocks, num_pages, Hq, Hkv, D, P, scale,
-        decay, num_splits, _dt(q), ws_ptr, 0 if workspace is None else workspace.nbytes, _ptr(err_flag),
-        _stream(stream))
+        need(lse, "lse", dev, torch.float32, (B, Hq)), in_ptr, out_ptr, B, max_blocks, num_pages, Hq, Hkv, D, P,
+        float(scale), float(decay), int(num_splits), _dt(q), ws_ptr, 0 if workspace is None else workspace.nbytes, _ptr(err_flag),
+        _stream(stream, dev))
     _check(st, "attn_decode_paged_weights")
     return out, lse, sums_out
 
@@ -512,7 +518,7 @@ def chunk_weights(q, k_pages, block_table, prefix_lens, lse, weight_sums, scale,
     if D2 != D:
         raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
     max_blocks = block_table.shape[1]
-    dev, dtype, need = torch.cuda.current_device() if q.is_cuda else -2, q.dtype, _fast_need
+    dev, dtype, need = _device_of(q), q.dtype, _fast_need
     q_ptr = need(q, "q", dev, None, None)
     sums = (B, Hkv, max_blocks * P)
     in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, torch.float32, sums)
@@ -525,8 +531,8 @@ def chunk_weights(q, k_pages, block_table, prefix_lens, lse, weight_sums, scale,
         need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
         need(prefix_lens, "prefix_lens", dev, torch.int32, (B,)),
         None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, torch.int32, (B,)),
-        need(lse, "lse", dev, torch.float32, (B, Hq, C)), in_ptr, out_ptr, B, C, window, max_blocks, num_pages, Hq, Hkv,
-        D, P, scale, decay, _dt(q), _ptr(err_flag), _stream(stream))
+        need(lse, "lse", dev, torch.float32, (B, Hq, C)), in_ptr, out_ptr, B, C, int(window), max_blocks, num_pages, Hq,
+        Hkv, D, P, float(scale), float(decay), _dt(q), _ptr(err_flag), _stream(stream, dev))
     _check(st, "attn_chunk_weights")
     return sums_out
 
@@ -538,7 +544,7 @@ def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_t
     num_pages, Hkv, P, D = k_pages.shape
     B, max_blocks = block_table.shape
     new_blocks = new_block_table.shape[1]
-    dev, need = torch.cuda.current_device() if k_pages.is_cuda else -2, _fast_need
+    dev, need, budget = _device_of(k_pages), _fast_need, int(budget)
     i32, f32 = torch.int32, torch.float32
     k_ptr = need(k_pages, "k_pages", dev, None, None)
     if kept is None:
@@ -554,7 +560,7 @@ def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_t
         need(new_block_table, "new_block_table", dev, i32, (B, new_blocks)),
         need(kept, "kept", dev, i32, (B, Hkv, max(budget, 0))), need(new_lens, "new_lens", dev, i32, (B,)),
         need(new_sums, "new_sums", dev, f32, (B, Hkv, new_blocks * P)), B, max_blocks, new_blocks, num_pages, Hkv, D, P,
-        budget, n_sink, n_recent, _dt(k_pages), _ptr(err_flag), _stream(stream))
+        budget, int(n_sink), int(n_recent), _dt(k_pages), _ptr(err_flag), _stream(stream, dev))
     _check(st, "attn_cache_evict")
     return kept, new_lens, new_sums
 
@@ -572,14 +578,14 @@ def linear(x, w, bias=None, activation="none", residual=None, out=None, err_flag
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r}, one of {sorted(ACTIVATIONS)}")
-    dev, dtype, need = torch.cuda.current_device() if x.is_cuda else -2, x.dtype, _fast_need
+    dev, dtype, need = _device_of(x), x.dtype, _fast_need
     x_ptr = need(x, "x", dev, None, None)
     if out is None:
         out = torch.empty((m, n), dtype=dtype, device=x.device)
     st = _pycall.attn_linear(
         x_ptr, need(w, "w", dev, dtype, (n, k)), None if bias is None else need(bias, "bias", dev, dtype, (n,)),
         None if residual is None else need(residual, "residual", dev, dtype, (m, n)), need(out, "out", dev, dtype, (m, n)),
-        m, n, k, act, _dt(x), _ptr(err_flag), _stream(stream))
+        m, n, k, act, _dt(x), _ptr(err_flag), _stream(stream, dev))
     _check(st, "attn_linear")
     return out
 

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, int
   const int tid = threadIdx.x;
   const int pairs = a.rotary_dim / 2;
   const int b = blockIdx.y, first = blockIdx.x * per_cta;
+  wait_for_stream();
   const int len = __ldg(a.prefix_lens + b);
   const int n = a.chunk_lens ? __ldg(a.chunk_lens + b) : a.chunk_len;
   const bool bad_n = n < 0 || n > a.chunk_len;
@@ -241,13 +242,13 @@ int launch_t(const AppendArgs& a, cudaStream_t stream) {
   // Few tokens: one per CTA of 256 threads, which puts most rows at work at once. Many: two per CTA
   // of 128 threads (one or four are 3 to 8 % slower, 256 or 64 threads 10 and 30 %).
   if ((int64_t)a.batch * a.chunk_len <= 16 * (int64_t)sms) {
-    append_kernel<T, D, 256><<<dim3((unsigned)a.chunk_len, (unsigned)a.batch), 256, 0, stream>>>(a, 1);
+    return check_launch(launch_overlapped(append_kernel<T, D, 256>, dim3((unsigned)a.chunk_len, (unsigned)a.batch), 256,
+                                          0, stream, 1, a, 1));
   } else {
     constexpr int kPer = 2;
-    append_kernel<T, D, 128>
-        <<<dim3((unsigned)((a.chunk_len + kPer - 1) / kPer), (unsigned)a.batch), 128, 0, stream>>>(a, kPer);
+    const dim3 grid((unsigned)((a.chunk_len + kPer - 1) / kPer), (unsigned)a.batch);
+    return check_launch(launch_overlapped(append_kernel<T, D, 128>, grid, 128, 0, stream, 1, a, kPer));
   }
-  return check_launch(cudaGetLastError());
 }
 
 }  // namespace

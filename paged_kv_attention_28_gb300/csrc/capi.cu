@@ -119,6 +119,9 @@ static SplitPlan plan_decode(int batch, int max_blocks, int n_qo_heads, int n_kv
   return plan_decode_splits(batch, max_blocks, n_kv_heads, num_splits, decode_ctas_per_sm(dtype, head_dim, G));
 }
 
+// Capacity per sequence up to which token indices rounded up to a tile fit 32 bits.
+constexpr long kMaxTokens = 1L << 30;
+
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Split partials: O [rows][S][D], LSE [rows][S].
@@ -495,6 +498,7 @@ int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_
   if (!aligned16(q) || !aligned16(k_pages)) return PKV_ERR_INVALID_ARG;
   const int G = n_qo_heads / n_kv_heads;
   if (dtype != PKV_BF16 || head_dim != 128 || page_size != 16 || 128 % G) return PKV_ERR_UNSUPPORTED;
+  if ((long)max_blocks_per_seq * page_size > kMaxTokens) return PKV_ERR_UNSUPPORTED;
   ChunkWeightsArgs a{q, k_pages, block_table, prefix_lens, chunk_lens, lse, sums_in, sums_out, batch, chunk_len,
                      window, max_blocks_per_seq, num_pages, n_qo_heads, n_kv_heads, head_dim, page_size, scale,
                      decay, err_flag};
@@ -537,8 +541,13 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
   if (!k_pages || !v_pages || !block_table || !kv_lens || !sums || !new_block_table || !kept || !new_lens || !new_sums)
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(sums)) return PKV_ERR_INVALID_ARG;
+  // (a head's outputs are written while other heads still read the inputs)
+  if (new_lens == kv_lens || new_sums == sums || kept == block_table || kept == new_block_table)
+    return PKV_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || page_size != 16) return PKV_ERR_UNSUPPORTED;
   if (batch > 65535 || n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  if ((long)max_blocks_per_seq * page_size > kMaxTokens || (long)new_max_blocks * page_size > kMaxTokens)
+    return PKV_ERR_UNSUPPORTED;
   EvictArgs a{k_pages, v_pages, block_table, kv_lens, sums, new_block_table, kept, new_lens, new_sums, batch,
               max_blocks_per_seq, new_max_blocks, num_pages, n_kv_heads, head_dim, page_size, budget, n_sink,
               n_recent, dtype, err_flag};

@@ -184,6 +184,7 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   auto share_of = [&](int steps) { return SPLIT ? (steps > rank ? (steps - rank + S - 1) >> s_log2 : 0) : steps; };
 
   int2* lens = reinterpret_cast<int2*>(smem + SM_LEN);
+  wait_for_stream();
   for (int b = threadIdx.x; b < a.batch && b < CLENS; b += CTHREADS) lens[b] = read_lens(a, b);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C_NBAR; ++i) {
@@ -570,24 +571,13 @@ int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream) {
     static FuncConfigured configured;
     if (!configured.ensure(reinterpret_cast<const void*>(chunk_weights_kernel<false>), C_SMEM)) return PKV_ERR_LAUNCH;
     const int grid = (int)(n_tiles * rows < sms ? n_tiles * rows : sms);
-    chunk_weights_kernel<false><<<grid, CTHREADS, C_SMEM, stream>>>(mq, mk, a, (int)n_tiles, 0);
-    return check_launch(cudaGetLastError());
+    return check_launch(
+        launch_overlapped(chunk_weights_kernel<false>, dim3((unsigned)grid), CTHREADS, C_SMEM, stream, 1, mq, mk, a, (int)n_tiles, 0));
   }
   static FuncConfigured configured;
   if (!configured.ensure(reinterpret_cast<const void*>(chunk_weights_kernel<true>), C_SMEM)) return PKV_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(n_tiles * rows << s_log2), 1, 1);
-  cfg.blockDim = dim3(CTHREADS, 1, 1);
-  cfg.dynamicSmemBytes = C_SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1u << s_log2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, chunk_weights_kernel<true>, mq, mk, a, (int)n_tiles, s_log2));
+  return check_launch(launch_overlapped(chunk_weights_kernel<true>, dim3((unsigned)(n_tiles * rows << s_log2)), CTHREADS, C_SMEM,
+                                        stream, 1 << s_log2, mq, mk, a, (int)n_tiles, s_log2));
 }
 
 }  // namespace pkv

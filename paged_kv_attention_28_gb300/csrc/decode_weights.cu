@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_weights_kernel(const De
   if ((int)blockIdx.x < merge_rows) {
     const int row = blockIdx.x;
     const int len = __ldg(a.d.kv_lens + row / a.d.n_qo_heads);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the decode is complete after this
+    wait_for_stream();  // (the decode)
     if (len < 0 || len > cap) return;
     const int n = splits_of(len);
     if (n < 2) return;  // the decode wrote the row
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_weights_kernel(const De
   const int64_t at = ((int64_t)b * a.d.n_kv_heads + g) * cap + t;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
   if (live) w = *reinterpret_cast<const float4*>(a.sums_in + at);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   if (!any) return;
   const int64_t row0 = (int64_t)b * a.d.n_qo_heads + (int64_t)g * G;
   float4 x[G];
@@ -113,16 +113,8 @@ int launch_finish(const DecodeWeightsArgs& a, cudaStream_t stream) {
   const int64_t rows = a.d.num_splits > 1 ? (int64_t)a.d.batch * a.d.n_qo_heads : 0;
   const int64_t grid = rows + tiles * a.d.n_kv_heads * a.d.batch;
   if (grid > 0x7fffffffL) return PKV_ERR_UNSUPPORTED;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(kFinishThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, finish_weights_kernel<T, D, G>, a, (int)rows, (int)tiles));
+  return check_launch(launch_overlapped(finish_weights_kernel<T, D, G>, dim3((unsigned)grid), kFinishThreads, 0, stream, 1, a,
+                                        (int)rows, (int)tiles));
 }
 
 template <typename T, int D>

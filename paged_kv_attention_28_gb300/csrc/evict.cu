@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
   const int b = blockIdx.y, h = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_stream();
   const int cap = a.max_blocks * a.page_size, new_cap = a.new_max_blocks * a.page_size;
   const int64_t row = (int64_t)b * a.n_kv_heads + h;
   const float* sums = a.sums + row * cap;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const EvictArgs 
   const int32_t* new_table = a.new_block_table + (int64_t)b * a.new_max_blocks;
   const uint32_t nan = a.dtype == PKV_F32 ? 0x7fc00000u : 0x7fc07fc0u;
   const int j0 = blockIdx.x * (GROUPS * kGatherRows) + group;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   int src[kGatherRows];
 #pragma unroll
   for (int u = 0; u < kGatherRows; ++u) {
@@ -302,16 +303,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const EvictArgs 
 template <int ROW>
 int launch_gather(const EvictArgs& a, cudaStream_t stream) {
   constexpr int TILE = kGatherThreads / (ROW / 16) * kGatherRows;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((a.budget + TILE - 1) / TILE), (unsigned)a.n_kv_heads, (unsigned)a.batch);
-  cfg.blockDim = dim3(kGatherThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, gather_kernel<ROW>, a));
+  const dim3 grid((unsigned)((a.budget + TILE - 1) / TILE), (unsigned)a.n_kv_heads, (unsigned)a.batch);
+  return check_launch(launch_overlapped(gather_kernel<ROW>, grid, kGatherThreads, 0, stream, 1, a));
 }
 
 }  // namespace
@@ -319,17 +312,18 @@ int launch_gather(const EvictArgs& a, cudaStream_t stream) {
 int launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const int64_t cap = (int64_t)a.max_blocks * a.page_size;
   const dim3 grid((unsigned)a.n_kv_heads, (unsigned)a.batch);
+  int rc;
   if (cap <= kShortTokens) {
-    select_kernel<true, 256><<<grid, 256, (size_t)((cap + 1023) / 1024) * 4096, stream>>>(a);
+    rc = check_launch(launch_overlapped(select_kernel<true, 256>, grid, 256, (size_t)((cap + 1023) / 1024) * 4096, stream, 1, a));
   } else if (cap <= kSmemTokens) {
     static FuncConfigured configured;
     if (!configured.ensure(reinterpret_cast<const void*>(select_kernel<true, 1024>), kSmemTokens * 4))
       return PKV_ERR_LAUNCH;
-    select_kernel<true, 1024><<<grid, 1024, (size_t)((cap + 4095) / 4096) * 16384, stream>>>(a);
+    rc = check_launch(
+        launch_overlapped(select_kernel<true, 1024>, grid, 1024, (size_t)((cap + 4095) / 4096) * 16384, stream, 1, a));
   } else {
-    select_kernel<false, 1024><<<grid, 1024, 0, stream>>>(a);
+    rc = check_launch(launch_overlapped(select_kernel<false, 1024>, grid, 1024, 0, stream, 1, a));
   }
-  const int rc = check_launch(cudaGetLastError());
   if (rc != PKV_OK) return rc;
   switch (a.head_dim * (a.dtype == PKV_F32 ? 4 : 2)) {
     case 128: return launch_gather<128>(a, stream);

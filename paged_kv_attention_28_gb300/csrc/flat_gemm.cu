@@ -144,6 +144,8 @@ flat_gemm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__
     misc->failed = 0;
     fence_mbar_init();
   }
+  // (launched overlapped; before tensor memory is taken: an earlier kernel may still need it)
+  if constexpr (EPI) wait_for_stream();
   if (warp == 0) {
     tmem_alloc(smem_u32(&misc->tmem_base), C::TMEM_COLS);
     tmem_relinquish();
@@ -343,6 +345,9 @@ int launch_fg(const FlatGemmArgs& p, const Epilogue& ep, const FlatGemmPlan& pla
   static FuncConfigured configured;
   if (!configured.ensure(reinterpret_cast<const void*>(flat_gemm_kernel<NP, EPI>), C::SMEM)) return PKV_ERR_LAUNCH;
   FgArgs a{static_cast<__nv_bfloat16*>(p.y), p.err_flag, p.m, p.n, p.k, plan.kc_per_cta, plan.n_kc, ep};
+  if constexpr (EPI)
+    return check_launch(launch_overlapped(flat_gemm_kernel<NP, EPI>, dim3((unsigned)plan.splits, (unsigned)plan.tiles, 1),
+                                          FG_THREADS, C::SMEM, stream, plan.splits, mw, mx, a));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)plan.splits, (unsigned)plan.tiles, 1);
   cfg.blockDim = dim3(FG_THREADS, 1, 1);

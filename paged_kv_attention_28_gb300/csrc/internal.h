@@ -75,6 +75,28 @@ struct FuncConfigured {
   bool ensure(const void* func, int smem_bytes);
 };
 
+// Launches a kernel that starts with griddepcontrol.wait: its CTAs may be placed, and do what needs no
+// earlier result, while the stream's previous kernel ends. cluster: CTAs per cluster along x.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                              A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Remembers the most recent failing CUDA call of this host thread (see
 // attn_last_cuda_error_string) and returns PKV_ERR_LAUNCH, or PKV_OK on success.
 int check_launch(cudaError_t e);

@@ -200,6 +200,8 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     misc->abort_ = 0;
     fence_mbar_init();
   }
+  // (before tensor memory is taken: an earlier kernel of the stream may still need it)
+  wait_for_stream();
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&misc->tmem_base))
                  : "memory");
@@ -373,19 +375,7 @@ template <int SUB>
 int launch_t(const CUtensorMap& mx, const CUtensorMap& mw, const LinArgs& a, int bn, unsigned grid, cudaStream_t stream) {
   static FuncConfigured configured;
   if (!configured.ensure(reinterpret_cast<const void*>(linear_kernel<SUB>), LinCfg<SUB>::SMEM)) return PKV_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(LTHREADS, 1, 1);
-  cfg.dynamicSmemBytes = LinCfg<SUB>::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return check_launch(cudaLaunchKernelEx(&cfg, linear_kernel<SUB>, mx, mw, a, bn));
+  return check_launch(launch_overlapped(linear_kernel<SUB>, dim3(grid), LTHREADS, LinCfg<SUB>::SMEM, stream, 2, mx, mw, a, bn));
 }
 
 constexpr int kWide = 224;  // tiles from this width take one block per stage

@@ -123,6 +123,11 @@ __device__ __forceinline__ void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// In a kernel launched with launch_overlapped: everything before it in the stream is complete, and its
+// writes are visible, after this. Tensor memory is allocated after it: a kernel that is still to
+// allocate its own would otherwise wait for one that waits for it.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void set_err(int32_t* err_flag, int bits) {
   if (err_flag) atomicOr(err_flag, bits);
 }

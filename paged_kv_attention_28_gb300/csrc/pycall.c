@@ -70,7 +70,7 @@ static int raw(PyObject* const* a, Py_ssize_t n, Py_ssize_t want, const char* na
     return 0;
   }
   for (Py_ssize_t i = 0; i < n; ++i) {
-    if (a[i] == Py_None || PyFloat_CheckExact(a[i])) continue;
+    if (a[i] == Py_None || PyFloat_Check(a[i])) continue;
     if (!PyLong_Check(a[i])) {
       PyErr_Format(PyExc_TypeError, "%s() argument %zd is a %s", name, i, Py_TYPE(a[i])->tp_name);
       return 0;
@@ -87,7 +87,7 @@ static int int_of(PyObject* o) {
   return v < INT_MIN || v > INT_MAX ? INT_MIN : (int)v;
 }
 static float float_of(PyObject* o) {
-  return PyFloat_CheckExact(o) ? (float)PyFloat_AS_DOUBLE(o) : PyLong_Check(o) ? (float)PyLong_AsLongLong(o) : 0.0f;
+  return PyFloat_Check(o) ? (float)PyFloat_AS_DOUBLE(o) : PyLong_Check(o) ? (float)PyLong_AsLongLong(o) : 0.0f;
 }
 
 #define PTR(i) ptr_of(a[i])

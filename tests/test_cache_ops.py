@@ -22,6 +22,7 @@ def b():
 
 P = ctypes.c_void_p(1 << 20)
 ODD = ctypes.c_void_p((1 << 20) + 4)
+P2, P3 = ctypes.c_void_p(1 << 21), ctypes.c_void_p(1 << 22)
 ODD1 = ctypes.c_void_p((1 << 20) + 1)
 
 
@@ -128,7 +129,7 @@ def test_decode_weights_workspace(b):
 
 
 def evict_args(b, **kw):
-    a = dict(kp=P, vp=P, bt=P, ln=P, s=P, nt=P, kept=P, nl=P, ns=P, batch=1, mb=8, nb=2, np=16, hkv=2, d=64, page=16,
+    a = dict(kp=P, vp=P, bt=P, ln=P, s=P, nt=P, kept=P3, nl=P3, ns=P3, batch=1, mb=8, nb=2, np=16, hkv=2, d=64, page=16,
              budget=32, sink=4, recent=8, dt=b.PKV_BF16)
     a.update(kw)
     return list(a.values()) + [None, None]
@@ -138,7 +139,8 @@ def evict_args(b, **kw):
     (dict(kp=None), -1), (dict(kept=None), -1), (dict(ns=None), -1), (dict(nt=None), -1), (dict(kp=ODD), -1), (dict(s=ODD), -1),
     (dict(budget=0), -1), (dict(budget=33), -1), (dict(sink=-1), -1), (dict(recent=-1), -1), (dict(sink=25), -1),
     (dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), -1), (dict(batch=-1), -1), (dict(mb=0), -1), (dict(nb=0), -1),
-    (dict(dt=5), -1), (dict(mb=1 << 28), -1), (dict(d=96), -2), (dict(page=32, budget=64), -2), (dict(batch=70000), -2),
+    (dict(dt=5), -1), (dict(mb=1 << 28), -1), (dict(mb=(1 << 26) + 1), -2), (dict(nl=P2, ln=P2), -1), (dict(s=P2, ns=P2), -1),
+    (dict(kept=P2, nt=P2), -1), (dict(kept=P2, bt=P2), -1), (dict(d=96), -2), (dict(page=32, budget=64), -2), (dict(batch=70000), -2),
     (dict(batch=0, kp=None), 0),
 ])
 def test_evict_refuses(b, bad, want):
@@ -156,7 +158,8 @@ def chunk_args(b, **kw):
     (dict(q=None), -1), (dict(lse=None), -1), (dict(si=None), -1), (dict(so=None), -1), (dict(kp=None), -1),
     (dict(q=ODD), -1), (dict(kp=ODD), -1), (dict(window=-1), -1), (dict(chunk=-1), -1), (dict(chunk=65), -1),
     (dict(scale=float("inf")), -1), (dict(decay=float("nan")), -1), (dict(hq=9), -1), (dict(dt=7), -1), (dict(mb=0), -1),
-    (dict(dt=0), -2), (dict(d=64), -2), (dict(page=8, mb=8), -2), (dict(hq=6), -2), (dict(batch=0, q=None), 0),
+    (dict(dt=0), -2), (dict(d=64), -2), (dict(page=8, mb=8), -2), (dict(hq=6), -2), (dict(mb=(1 << 26) + 1), -2),
+    (dict(batch=0, q=None), 0),
     (dict(chunk=0, q=None), 0),
 ])
 def test_chunk_weights_refuses(b, bad, want):

@@ -97,6 +97,10 @@ def test_many_items_per_cta(b):
     check(b, [37 * i % 1500 for i in range(48)], 24, 16, 8)
 
 
+def test_more_sequences_than_lengths_kept_in_shared_memory(b):
+    check(b, [(7 * i) % 23 for i in range(2100)], 2, 1, 1)
+
+
 def test_bad_lengths_and_pages(b):
     q, kp, table, pl, lse, sums, n = make(5, [100, 200, 300], 40, 8, 2)
     clean = b.chunk_weights(q.cuda(), kp.cuda(), table.cuda(), pl.cuda(), lse.cuda(), sums.cuda(), 0.1).cpu()
