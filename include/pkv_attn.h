@@ -460,7 +460,8 @@ int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_
  * for t < kv_lens[b]; slots at or past the length are neither read nor written, so the sums of
  * the newest token must have been set (to 0) before. sums_out may be sums_in (in place), and
  * must not overlap it otherwise. decay is finite (1: plain accumulation). out, lse, splits and
- * errors are as for attn_decode_paged; a row that came out NaN makes its group's sums NaN, and
+ * errors are as for attn_decode_paged (out is closer to the exact value than that call's where
+ * the tensor cores take the weights: two bf16 parts of each, not one); a row that came out NaN makes its group's sums NaN, and
  * a bad length leaves the sequence's sums as they were. workspace: at least
  * attn_decode_weights_workspace_size bytes, 256-byte aligned: the split partials, the call's
  * logits (fp32 [batch][n_qo_heads][max_blocks_per_seq * page_size]) and log-sum-exps.

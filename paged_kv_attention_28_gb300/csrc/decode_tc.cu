@@ -562,7 +562,10 @@ __device__ __forceinline__ void convert_fp8(const DecodeArgs& a, unsigned char* 
 // f16 after a per-row power-of-two scaling, and both products take f16 operands.
 //
 // LOGITS: every key's logits, in base-2 units, also go to a.logits [batch][n_qo_heads][max_blocks
-// * 16] in fp32; 128 keys of a head are one contiguous run of stores by the softmax threads.
+// * 16] in fp32; 128 keys of a head are one contiguous run of stores by the softmax threads. The
+// weights then enter the V product as two bf16 parts each, in the group's rows of P^T and in the
+// padding rows after them (2 G <= 16), at no further product: the sum of both rows of O^T has the
+// weights to 2^-17 instead of 2^-9, so that the output is off by its own rounding alone.
 template <int G, bool UNIFIED, bool CASCADE, bool FP8, bool LOGITS = false>
 __global__ void __launch_bounds__(TcL<FP8>::THREADS, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -982,7 +985,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
           tmem_ld16(tmem + lane_addr + COL_O + qb * NQ, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < G; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
+          for (int h = 0; h < G; ++h) {
+            o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
+            if constexpr (LOGITS) o[G + h] = __float_as_uint(__uint_as_float(o[G + h]) * alpha[h]);
+          }
           tmem_st16(tmem + lane_addr + COL_O + qb * NQ, o);
           tmem_st_wait();
         }
@@ -998,6 +1004,14 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                                                                    ((chunk ^ (h & 7)) << 4) + (within & 7) * 2);
           // E4M3 pools: the weight times its page's V scale, in f16 (the V tile holds the codes)
           *dstp = FP8 ? __half_as_ushort(__float2half_rn(p * vsc)) : __bfloat16_as_ushort(__float2bfloat16_rn(p));
+          if constexpr (LOGITS) {  // what that rounding left, in row G + h
+            static_assert(2 * G <= NQ && !FP8, "padding rows for the second part");
+            constexpr int kRow = 128, kGroup = 1024;
+            const int row = G + h;
+            unsigned short* low = reinterpret_cast<unsigned short*>(pbuf + (row >> 3) * kGroup + (row & 7) * kRow +
+                                                                    ((chunk ^ (row & 7)) << 4) + (within & 7) * 2);
+            *low = __bfloat16_as_ushort(__float2bfloat16_rn(p - __bfloat162float(__float2bfloat16_rn(p))));
+          }
         }
         if (valid < TK) {
           // masked keys enter PV as 0 x V: the V rows past the sequence (not the caller's
@@ -1104,6 +1118,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           o[h] = __uint_as_float(r[h]);
+          if constexpr (LOGITS) o[h] += __uint_as_float(r[G + h]);
           mh[h] = stats[(qb * NQ + h) * 2];
           lh[h] = stats[(qb * NQ + h) * 2 + 1];
         }
