@@ -111,8 +111,12 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
-# The checks and calls of the operators whose small calls are bound by the host (csrc/pycall.c).
+# The checks and calls of the operators whose small calls are bound by the host (csrc/pycall.cpp).
 from . import _pycall  # noqa: E402  (needs the library)
+
+if _pycall.torch_version.split(".")[:2] != torch.__version__.split(".")[:2]:
+    raise ImportError(f"_pycall.so was built for PyTorch {_pycall.torch_version}, this is {torch.__version__}: "
+                      "build it again with `python -m paged_kv_attention_28_gb300.build --force`")
 
 
 def status_string(status: int) -> str:
@@ -141,6 +145,7 @@ def _ptr(t):
 
 # The raw handle of a device's current stream, without building a torch.cuda.Stream (2 us).
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None, device=None):
@@ -154,7 +159,7 @@ def _stream(stream=None, device=None):
 
 def _device_of(t: torch.Tensor) -> int:
     """The current device, where every tensor of a call has to be (-2 for a host tensor: no device)."""
-    return torch.cuda.current_device() if t.is_cuda else -2
+    return _current_device() if t.is_cuda else -2
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
@@ -401,6 +406,9 @@ _fast_need = _pycall.need
 
 def _token_rows(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
     """Checks ``[B, C, H, D]`` whose head rows are contiguous per token; the token stride."""
+    step = _pycall.rows(t, dev, dtype, shape)
+    if step >= 0:
+        return step
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
     if t.dtype is not dtype:

@@ -188,3 +188,27 @@ def test_empty_calls_do_nothing(b):
     c = Case(16, 2, 4, 8, 4, 64, "f32", [3, 20], 64, chunk_lens=[0, 0])
     out, kp, vp, err = c.call(b)
     assert err == 0 and torch.equal(out, c.q_out) and torch.equal(kp, c.k_pages) and torch.equal(vp, c.v_pages)
+
+
+def test_native_checks_of_real_tensors():
+    """The checks that read a tensor directly agree with what the tensor says of itself."""
+    from paged_kv_attention_28_gb300 import _pycall
+    x = torch.zeros(3, 5, 8, 16, dtype=torch.bfloat16, device="cuda")
+    bf, dims = torch.bfloat16, (3, 5, 8, 16)
+    for d, s in ((bf, dims), (None, None), (bf, None), (None, x.shape)):
+        assert _pycall.need(x, "x", 0, d, s) == x.data_ptr()
+    assert _pycall.need(x[1:], "x", 0, bf, (2, 5, 8, 16)) == x[1:].data_ptr()
+    assert _pycall.need(x[:0], "x", 0, bf, (0, 5, 8, 16)) == x[:0].data_ptr()
+    for t, dev, d, s in ((x, 1, bf, dims), (x, 0, torch.float16, dims), (x, 0, bf, (3, 5, 8, 8)), (x, 0, bf, (3, 5, 128)),
+                         (x, 0, bf, (3, 5, 8, 1 << 70)), (x[:, ::2], 0, bf, None), (x.transpose(0, 1), 0, bf, None)):
+        with pytest.raises(ValueError):
+            _pycall.need(t, "x", dev, d, s)
+    fused = torch.zeros(3, 5, 24, 16, dtype=torch.bfloat16, device="cuda")
+    assert _pycall.rows(x, 0, bf, dims) == 128
+    assert _pycall.rows(fused[:, :, 8:16], 0, bf, dims) == 24 * 16
+    assert _pycall.rows(fused[:, :1, 8:16], 0, bf, (3, 1, 8, 16)) == 5 * 24 * 16
+    assert _pycall.rows(fused[:1, :1, 8:16], 0, bf, (1, 1, 8, 16)) == 8 * 16
+    for t, s in ((fused[:, :4, 8:16], (3, 4, 8, 16)), (fused[:, :, 8:16:2], (3, 5, 4, 16)), (fused[..., :8], (3, 5, 24, 8)),
+                 (x, (3, 5, 16, 8))):
+        assert _pycall.rows(t, 0, bf, s) == -1
+    assert _pycall.rows(x, 1, bf, dims) == -1 and _pycall.rows(x, 0, torch.float16, dims) == -1
