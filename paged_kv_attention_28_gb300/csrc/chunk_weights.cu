@@ -24,7 +24,7 @@
 // of the CTAs backwards (135 to 108 us against a plain stride). With fewer items than half the SMs
 // an item's steps are shared by a cluster of 2 to 8 CTAs, whose partial sums are added in rank
 // order through distributed shared memory.
-// Warps: 0 and 2 TMA producers (a ring of three K tiles, page by page, and one of three Q tiles), 1
+// Warps: 0 and 2 TMA producers (a ring of four K tiles, page by page, and one of two Q tiles), 1
 // and 3 MMA issuers of the two key tiles, 4..11 and 12..19 their exponentials and sums. S^T is
 // double-buffered per tile: all 512 TMEM columns.
 #include <cuda.h>
@@ -51,10 +51,14 @@ constexpr int CN = 128;                // columns (queries x heads of the group)
 constexpr int KSTG = 128 * CD * 2;
 constexpr int QSTG = CN * CD * 2;      // one Q stage, 32 KiB: two 64-dim halves
 constexpr int HALF = 128 * 128;        // [128 rows][128 bytes]
-constexpr int NKS = 3, NQS = 3;
+constexpr int NKS = 4, NQS = 2;
+// An item takes two K stages in turn, one for each issuer. A wait by parity cannot tell a phase from the
+// one two before, so whoever waits on a barrier has to see all of its phases: with an even number a
+// stage is always the same issuer's.
+static_assert(NKS % 2 == 0, "a K stage belongs to one issuer");
 constexpr int CTHREADS = 640;
 // barriers
-constexpr int C_KF = 0, C_KE = 3, C_QF = 6, C_QE = 9, C_SF = 12, C_SE = 16, C_DR = 20, C_HF = 21,
+constexpr int C_KF = 0, C_KE = C_KF + NKS, C_QF = C_KE + NKS, C_QE = C_QF + NQS, C_SF = C_QE + NQS, C_SE = C_SF + 4, C_DR = C_SE + 4, C_HF = C_DR + 1,
               C_NBAR = C_HF + 8 * 3;
 constexpr int CLENS = 2048;            // sequences whose lengths are kept in shared memory
 constexpr int CWARPS = 16;             // exponential warps, four .. nineteen

@@ -203,6 +203,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
   // (before tensor memory is taken: an earlier kernel of the stream may still need it)
   wait_for_stream();
   if (warp == 0) {
+    __syncwarp();  // the lanes converge after the barriers' initialisation
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&misc->tmem_base))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");

@@ -154,3 +154,42 @@ def test_chunk_weights_in_a_graph(b):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, call())
+
+
+def test_dozens_of_items_per_cta_from_cold_memory(b):
+    """Long caches under a short window: a CTA's rings of tiles turn over many times while pages come late and out of
+    order. Every call gives the same bits, and they are right."""
+    B, prefix, chunk, hq, hkv, scale = 16, 8192, 40, 32, 8, 128 ** -0.5
+    g = torch.Generator(device="cuda").manual_seed(5)
+    blocks = (prefix + chunk + 15) // 16
+    table = torch.randperm(B * blocks, device="cuda", generator=g).to(torch.int32).view(B, blocks)
+    kp = torch.randn(B * blocks, hkv, 16, 128, device="cuda", generator=g, dtype=torch.bfloat16)
+    q = torch.randn(B, chunk, hq, 128, device="cuda", generator=g, dtype=torch.bfloat16)
+    pl = torch.tensor([prefix - 100 * i for i in range(B)], dtype=torch.int32, device="cuda")
+    lse = 9.0 + torch.rand(B, hq, chunk, device="cuda", generator=g)
+    sums = torch.rand(B, hkv, blocks * 16, device="cuda", generator=g)
+    flush = torch.zeros(192 << 20, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for window in (1, 32):
+        got = []
+        for _ in range(6):
+            flush.zero_()
+            got.append(b.chunk_weights(q, kp, table, pl, lse, sums, scale, sums_out=torch.full_like(sums, 7.0), window=window,
+                                       err_flag=err))
+        assert int(err) == 0
+        assert all(torch.equal(got[0], x) for x in got[1:])
+        for i in range(B):
+            n = int(pl[i]) + chunk
+            keys = kp[table[i].long()].permute(1, 0, 2, 3).reshape(hkv, -1, 128)[:, :n].double()
+            z = torch.einsum("qhgd,htd->hqgt", q[i, chunk - window:].double().view(window, hkv, hq // hkv, 128), keys) * scale
+            seen = torch.arange(n, device="cuda") <= n - window + torch.arange(window, device="cuda")[:, None]
+            w = (z - lse[i, :, chunk - window:].double().view(hkv, hq // hkv, window).permute(0, 2, 1)[..., None]).exp()
+            w = (w * seen[None, :, None]).sum((1, 2))
+            # the product's 128 additions, the exponent's roundings, the sum over the columns, the final addition
+            top = scale * float(q[i].double().abs().amax() * keys.abs().sum(-1).amax())
+            e = 2.0 ** -23 * (128 * top + 4 * (top + 10.0))
+            want = w + sums[i, :, :n].double()
+            bar = w * (2 * e + 2.0 ** -20 + (window * hq // hkv + 8) * 2.0 ** -24) + (want + sums[i, :, :n].double()) * 2.0 ** -23
+            off = (got[0][i, :, :n].double() - want).abs()
+            assert bool((off <= bar).all()), (window, i, float((off / bar).max()))
+            assert bool((got[0][i, :, n:] == 7.0).all())
