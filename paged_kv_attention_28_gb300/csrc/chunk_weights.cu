@@ -60,10 +60,10 @@ constexpr int CTHREADS = 640;
 // barriers
 constexpr int C_KF = 0, C_KE = C_KF + NKS, C_QF = C_KE + NKS, C_QE = C_QF + NQS, C_SF = C_QE + NQS, C_SE = C_SF + 4, C_DR = C_SE + 4, C_HF = C_DR + 1,
               C_NBAR = C_HF + 8 * 3;
-constexpr int CLENS = 2048;            // sequences whose lengths are kept in shared memory
+constexpr int CITEMS = 512;            // items of a CTA
 constexpr int CWARPS = 16;             // exponential warps, four .. nineteen
-constexpr int SM_K = 0, SM_Q = SM_K + NKS * KSTG, SM_L = SM_Q + NQS * QSTG, SM_X = SM_L + CWARPS * CN * 4, SM_LEN = SM_X + 4 * CK * 4,
-              SM_BAR = SM_LEN + CLENS * 8,
+constexpr int SM_K = 0, SM_Q = SM_K + NKS * KSTG, SM_L = SM_Q + NQS * QSTG, SM_X = SM_L + CWARPS * CN * 4, SM_ITEM = SM_X + 4 * CK * 4,
+              SM_BAR = SM_ITEM + CITEMS * 32,
               SM_MISC = SM_BAR + C_NBAR * 8, C_SMEM = SM_MISC + 16 + 1024;
 static_assert(C_SMEM <= 232448, "shared memory per CTA");
 constexpr float kL2e = 1.4426950408889634f;
@@ -74,70 +74,36 @@ struct CMisc {
 };
 
 // One item: the keys it covers and the steps of columns that see any of them.
-struct Item {
+struct alignas(16) Item {
   int b, hk, key0;
-  int total;   // keys of the sequence after the chunk; 0: nothing to do; -1: bad lengths
-  int prefix;
-  int q_begin, q_end;  // queries that count and see a key of the item: [q_begin, q_end)
-  int steps;
+  int steps;    // 0: none (the sums only decay), -1: nothing to do
+  int prefix, n;  // cached and new tokens of the sequence
+  int q_begin;  // queries that count and see a key of the item: [q_begin, n)
+  int row;      // b, hk as one index
+  __device__ __forceinline__ int total() const { return prefix + n; }
 };
+static_assert(sizeof(Item) == 32, "item list");
 
-// Where a CTA stands in the items: key tiles slowest, then sequences, then KV heads. CTA i of P
-// takes items i, 2P - 1 - i, 2P + i, ...; the two distances are added in turn in mixed radix, so
-// that no role divides by run-time sizes for each item.
-struct Cursor {
-  int tile, b, hk;
-  int d_tile[2], d_b[2], d_hk[2], odd;
-  __device__ __forceinline__ Cursor(const ChunkWeightsArgs& a, int i, int P) : odd(0) {
-    const int rows = a.batch * a.n_kv_heads;
-    auto split = [&](int x, int& t, int& b_, int& h) {
-      t = x / rows;
-      b_ = x % rows / a.n_kv_heads;
-      h = x % rows % a.n_kv_heads;
-    };
-    split(i, tile, b, hk);
-    split(2 * P - 1 - 2 * i, d_tile[0], d_b[0], d_hk[0]);
-    split(2 * i + 1, d_tile[1], d_b[1], d_hk[1]);
-  }
-  __device__ __forceinline__ void next(const ChunkWeightsArgs& a) {
-    hk += odd ? d_hk[1] : d_hk[0];
-    b += odd ? d_b[1] : d_b[0];
-    tile += odd ? d_tile[1] : d_tile[0];
-    if (hk >= a.n_kv_heads) hk -= a.n_kv_heads, ++b;
-    if (b >= a.batch) b -= a.batch, ++tile;
-    odd ^= 1;
-  }
-};
-
-// A sequence's cached and new tokens; the new ones are -1 where the lengths are bad.
-__device__ __forceinline__ int2 read_lens(const ChunkWeightsArgs& a, int b) {
-  const int64_t prefix = __ldg(a.prefix_lens + b);
-  const int64_t n = a.chunk_lens ? __ldg(a.chunk_lens + b) : a.chunk_len;
-  const bool bad = prefix < 0 || n < 0 || n > a.chunk_len || prefix + n > (int64_t)a.max_blocks * a.page_size;
-  return make_int2((int)prefix, bad ? -1 : (int)n);
-}
-
-__device__ __forceinline__ Item make_item(const ChunkWeightsArgs& a, const int2* lens, const Cursor& c, int qpt_log2) {
+__device__ __forceinline__ Item make_item(const ChunkWeightsArgs& a, int index, int qpt_log2) {
+  const int rows = a.batch * a.n_kv_heads;
   Item it{};
-  it.key0 = c.tile * CK;
-  it.b = c.b;
-  it.hk = c.hk;
-  const int2 len = c.b < CLENS ? lens[c.b] : read_lens(a, c.b);
-  const int prefix = len.x, n = len.y;
-  if (n < 0) {
-    it.total = -1;
+  it.row = index % rows;
+  it.b = it.row / a.n_kv_heads;
+  it.hk = it.row % a.n_kv_heads;
+  it.key0 = index / rows * CK;
+  it.steps = -1;
+  const int64_t prefix = __ldg(a.prefix_lens + it.b);
+  const int64_t n = a.chunk_lens ? __ldg(a.chunk_lens + it.b) : a.chunk_len;
+  if (prefix < 0 || n < 0 || n > a.chunk_len || prefix + n > (int64_t)a.max_blocks * a.page_size) {
+    if (it.hk == 0 && it.key0 == 0) set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
     return it;
   }
-  it.total = prefix + n;
-  it.prefix = prefix;
-  if (it.key0 >= it.total) {
-    it.total = 0;
-    return it;
-  }
-  const int first = a.window > 0 && a.window < n ? n - a.window : 0;
+  it.prefix = (int)prefix;
+  it.n = (int)n;
+  if (it.key0 >= it.total()) return it;
+  const int first = a.window > 0 && a.window < it.n ? it.n - a.window : 0;
   it.q_begin = max(first, it.key0 - it.prefix);
-  it.q_end = n;
-  it.steps = it.q_end > it.q_begin ? (it.q_end - it.q_begin + (1 << qpt_log2) - 1) >> qpt_log2 : 0;
+  it.steps = it.n > it.q_begin ? (it.n - it.q_begin + (1 << qpt_log2) - 1) >> qpt_log2 : 0;
   return it;
 }
 
@@ -168,7 +134,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 template <bool SPLIT>
 __global__ void __launch_bounds__(CTHREADS, 1)
 chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const ChunkWeightsArgs a, int n_tiles, int s_log2) {
+                     const ChunkWeightsArgs a, int n_items, int s_log2) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
@@ -187,9 +153,14 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   // steps of an item that this CTA takes
   auto share_of = [&](int steps) { return SPLIT ? (steps > rank ? (steps - rank + S - 1) >> s_log2 : 0) : steps; };
 
-  int2* lens = reinterpret_cast<int2*>(smem + SM_LEN);
+  // The CTA's items, worked out by all threads at once, so that the warps below only read them. CTA i
+  // of P takes i, 2P - 1 - i, 2P + i, ...
+  Item* items = reinterpret_cast<Item*>(smem + SM_ITEM);
+  const int round = 2 * ctas, back = round - 1 - cta;
+  const int count = n_items / round * 2 + (cta < n_items % round) + (back < n_items % round);
   wait_for_stream();
-  for (int b = threadIdx.x; b < a.batch && b < CLENS; b += CTHREADS) lens[b] = read_lens(a, b);
+  for (int j = threadIdx.x; j < count; j += CTHREADS)
+    items[j] = make_item(a, (j >> 1) * round + (j & 1 ? back : cta), qpt_log2);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C_NBAR; ++i) {
       int cnt = 1;
@@ -227,9 +198,9 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   auto my_key = [&](const Item& it, int t) {
     Mine m{};
     const int key = it.key0 + t;
-    m.live = it.total > 0 && key < it.total;
+    m.live = key < it.total();
     if (m.live) {
-      m.at = ((int64_t)it.b * a.n_kv_heads + it.hk) * ((int64_t)a.max_blocks * a.page_size) + key;
+      m.at = (int64_t)it.row * (a.max_blocks * a.page_size) + key;
       m.before = a.sums_in[m.at];
       m.page = __ldg(a.block_table + (int64_t)it.b * a.max_blocks + key / 16);
     }
@@ -256,29 +227,25 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       // first page again (their keys are not written), a bad entry page 0 (its keys become NaN).
       // The next item's entries are asked for before this item's copies wait for room.
       auto entry = [&](const Item& it) {
-        const int pages = min(CK / 16, (it.total - it.key0 + 15) / 16);
+        const int pages = min(CK / 16, (it.total() - it.key0 + 15) / 16);
         return lane < 16 && it.steps > 0
                    ? __ldg(a.block_table + (int64_t)it.b * a.max_blocks + it.key0 / 16 + (lane < pages ? lane : 0))
                    : 0;
       };
-      Cursor at(a, cta, ctas);
       Item next{};
       int next_phys = 0;
-      bool more = at.tile < n_tiles;
-      if (more) {
-        next = make_item(a, lens, at, qpt_log2);
+      if (count > 0) {
+        next = items[0];
         next_phys = entry(next);
       }
-      while (ok && more) {
+      for (int j = 0; ok && j < count; ++j) {
         const Item it = next;
         int phys = next_phys;
-        at.next(a);
-        more = at.tile < n_tiles;
-        if (more) {
-          next = make_item(a, lens, at, qpt_log2);
+        if (j + 1 < count) {
+          next = items[j + 1];
           next_phys = entry(next);
         }
-        if (it.steps == 0) continue;
+        if (it.steps <= 0) continue;
         if (__any_sync(0xffffffffu, *aborted)) {
           ok = false;
           break;
@@ -307,8 +274,8 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       __syncwarp();
       uint32_t qc = 0;
       bool ok = true;
-      for (Cursor at(a, cta, ctas); ok && at.tile < n_tiles; at.next(a)) {
-        const Item it = make_item(a, lens, at, qpt_log2);
+      for (int j = 0; ok && j < count; ++j) {
+        const Item it = items[j];
         if (__any_sync(0xffffffffu, *aborted)) ok = false;
         for (int s = rank; ok && s < it.steps; s += S, ++qc) {
           const uint32_t qs = qc % NQS;
@@ -336,9 +303,9 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       const uint64_t dq0 = smem_desc(sb + SM_Q, 16, 1024, kSwizzle128B);
       uint32_t kt = tile, qc = 0;  // this tile's place in the K ring, steps so far
       bool ok = true;
-      for (Cursor at(a, cta, ctas); ok && at.tile < n_tiles; at.next(a)) {
-        const Item it = make_item(a, lens, at, qpt_log2);
-        if (it.steps == 0) continue;
+      for (int j = 0; ok && j < count; ++j) {
+        const Item it = items[j];
+        if (it.steps <= 0) continue;
         const uint32_t ks = kt % NKS;
         const uint64_t dk = dk0 + (uint64_t)((ks * KSTG) >> 4);
         for (int s = rank; ok && s < it.steps; s += S, ++qc) {
@@ -390,38 +357,35 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     auto lse_of = [&](const Item& it, int s, float (&v)[LC]) {
       if (s >= it.steps) return;
       const int q0 = it.q_begin + (s << qpt_log2);
-      const float* rows = a.lse + ((int64_t)it.b * a.n_qo_heads + it.hk * G) * a.chunk_len + q0;
+      const float* rows = a.lse + (int64_t)(it.row << g_log2) * a.chunk_len + q0;
 #pragma unroll
       for (int k = 0; k < LC; ++k) {
         const int col = 32 * k + lane, query = col >> g_log2;
-        v[k] = q0 + query < it.q_end ? __ldg(rows + (int64_t)(col & (G - 1)) * a.chunk_len + query) : 0.0f;
+        v[k] = q0 + query < it.n ? __ldg(rows + (int64_t)(col & (G - 1)) * a.chunk_len + query) : 0.0f;
       }
     };
     // look() goes on to the next item that these warps have a part in, and asks for its old sums,
     // table entries and first log-sum-exps, before the steps of the one at hand.
-    Cursor at(a, cta, ctas);
+    int at = 0;
     Item it{};
-    int count = 0;       // steps of the item that are this CTA's
+    int steps = 0;         // steps of the item that are this CTA's
     uint32_t next_qc = 0;  // steps before it
     bool more = true, finish = false;
     Mine mine{};
     float ahead[LC] = {};
     auto look = [&]() {
-      for (;; at.next(a)) {
-        next_qc += count;
-        count = 0;
-        more = at.tile < n_tiles;
+      for (;; ++at) {
+        next_qc += steps;
+        steps = 0;
+        more = at < count;
         if (!more) return;
-        it = make_item(a, lens, at, qpt_log2);
-        if (it.total <= 0) {
-          if (it.total < 0 && t == 0 && half == 0 && it.key0 == 0 && it.hk == 0) set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
-          continue;
-        }
-        count = share_of(it.steps);
-        if (count != 1 || half == (int)(next_qc & 1)) break;
+        it = items[at];
+        if (it.steps < 0) continue;
+        steps = share_of(it.steps);
+        if (steps != 1 || half == (int)(next_qc & 1)) break;
       }
-      at.next(a);
-      finish = count == 1 || half == 0;
+      ++at;
+      finish = steps == 1 || half == 0;
       if (finish) mine = my_key(it, t);
       lse_of(it, rank + (int)((half ^ next_qc) & 1) * S, ahead);
     };
@@ -430,7 +394,7 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     while (more) {
       const Item now = it;
       const Mine my = mine;
-      const int n_steps = count;
+      const int n_steps = steps;
       const uint32_t qc = next_qc;
       const bool fin = finish;
       float v[LC];
@@ -451,7 +415,7 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         tc_fence_after();
         const int q0 = now.q_begin + s * qpt;
         // columns [lo, hi) count: the causal bound and the end of the chunk
-        const int lo = (key - now.prefix - q0) * G, hi = min(CN, (now.q_end - q0) * G);
+        const int lo = (key - now.prefix - q0) * G, hi = min(CN, (now.n - q0) * G);
         const bool whole = __all_sync(0xffffffffu, lo <= 0) && hi == CN;
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -508,9 +472,9 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     const int share = CK / S, t = rank * share + (int)threadIdx.x;
     if ((int)threadIdx.x < share) {
-      const Item it = make_item(a, lens, Cursor(a, cta, ctas), qpt_log2);
+      const Item it = items[0];
       const Mine my = my_key(it, t);
-      if (my.live) {
+      if (it.steps >= 0 && my.live) {
         float total = 0.0f;
         for (int r = 0; r < S; ++r) {
           uint32_t addr;
@@ -572,16 +536,18 @@ int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream) {
   int s_log2 = 0;
   while (s_log2 < 3 && (2 << s_log2) <= steps && (n_tiles * rows << (s_log2 + 1)) <= sms) ++s_log2;
   if (s_log2 == 0) {
+    // a CTA per SM, more where the list of one cannot hold its share
+    const int64_t waves = (n_tiles * rows + (int64_t)sms * (CITEMS - 2) - 1) / ((int64_t)sms * (CITEMS - 2));
     static FuncConfigured configured;
     if (!configured.ensure(reinterpret_cast<const void*>(chunk_weights_kernel<false>), C_SMEM)) return PKV_ERR_LAUNCH;
-    const int grid = (int)(n_tiles * rows < sms ? n_tiles * rows : sms);
+    const int64_t grid = n_tiles * rows < sms * waves ? n_tiles * rows : sms * waves;
     return check_launch(
-        launch_overlapped(chunk_weights_kernel<false>, dim3((unsigned)grid), CTHREADS, C_SMEM, stream, 1, mq, mk, a, (int)n_tiles, 0));
+        launch_overlapped(chunk_weights_kernel<false>, dim3((unsigned)grid), CTHREADS, C_SMEM, stream, 1, mq, mk, a, (int)(n_tiles * rows), 0));
   }
   static FuncConfigured configured;
   if (!configured.ensure(reinterpret_cast<const void*>(chunk_weights_kernel<true>), C_SMEM)) return PKV_ERR_LAUNCH;
   return check_launch(launch_overlapped(chunk_weights_kernel<true>, dim3((unsigned)(n_tiles * rows << s_log2)), CTHREADS, C_SMEM,
-                                        stream, 1 << s_log2, mq, mk, a, (int)n_tiles, s_log2));
+                                        stream, 1 << s_log2, mq, mk, a, (int)(n_tiles * rows), s_log2));
 }
 
 }  // namespace pkv

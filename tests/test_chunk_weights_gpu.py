@@ -193,3 +193,25 @@ def test_dozens_of_items_per_cta_from_cold_memory(b):
             off = (got[0][i, :, :n].double() - want).abs()
             assert bool((off <= bar).all()), (window, i, float((off / bar).max()))
             assert bool((got[0][i, :, n:] == 7.0).all())
+
+
+def test_more_items_than_the_list_of_one_cta_per_sm(b):
+    """5000 sequences of a page with 16 KV heads: 80000 items, which take more CTAs than the device has SMs."""
+    B, h, scale = 5000, 16, 128 ** -0.5
+    g = torch.Generator(device="cuda").manual_seed(8)
+    table = torch.randperm(B, device="cuda", generator=g).to(torch.int32).view(B, 1)
+    kp = torch.randn(B, h, 16, 128, device="cuda", generator=g, dtype=torch.bfloat16)
+    q = torch.randn(B, 1, h, 128, device="cuda", generator=g, dtype=torch.bfloat16)
+    pl = (torch.arange(B, device="cuda") % 16).to(torch.int32)
+    lse = 3.0 + torch.rand(B, h, 1, device="cuda", generator=g)
+    sums = torch.rand(B, h, 16, device="cuda", generator=g)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = b.chunk_weights(q, kp, table, pl, lse, sums, scale, sums_out=torch.full_like(sums, 7.0), err_flag=err)
+    assert int(err) == 0
+    keys = kp[table[:, 0].long()].double()
+    w = (torch.einsum("bhd,bhtd->bht", q[:, 0].double(), keys) * scale - lse.double()).exp()
+    top = scale * float(q.double().abs().amax() * keys.abs().sum(-1).amax())
+    bar = w * (2.0 ** -22 * (128 * top + 4 * (top + 4.0)) + 2.0 ** -20) + (w + 2 * sums.double()) * 2.0 ** -23
+    live = (torch.arange(16, device="cuda") <= pl[:, None])[:, None].expand_as(w)
+    off = (got.double() - (w + sums.double())).abs()
+    assert bool((off <= bar)[live].all()) and bool((got[~live] == 7.0).all())
