@@ -60,10 +60,10 @@ constexpr int CTHREADS = 640;
 // barriers
 constexpr int C_KF = 0, C_KE = C_KF + NKS, C_QF = C_KE + NKS, C_QE = C_QF + NQS, C_SF = C_QE + NQS, C_SE = C_SF + 4, C_DR = C_SE + 4, C_HF = C_DR + 1,
               C_NBAR = C_HF + 8 * 3;
-constexpr int CITEMS = 512;            // items of a CTA
+constexpr int CITEMS = 256;            // items of a CTA
 constexpr int CWARPS = 16;             // exponential warps, four .. nineteen
 constexpr int SM_K = 0, SM_Q = SM_K + NKS * KSTG, SM_L = SM_Q + NQS * QSTG, SM_X = SM_L + CWARPS * CN * 4, SM_ITEM = SM_X + 4 * CK * 4,
-              SM_BAR = SM_ITEM + CITEMS * 32,
+              SM_BAR = SM_ITEM + CITEMS * 64,
               SM_MISC = SM_BAR + C_NBAR * 8, C_SMEM = SM_MISC + 16 + 1024;
 static_assert(C_SMEM <= 232448, "shared memory per CTA");
 constexpr float kL2e = 1.4426950408889634f;
@@ -73,37 +73,39 @@ struct CMisc {
   int abort_;
 };
 
-// One item: the keys it covers and the steps of columns that see any of them.
+// One item, 256 keys and the queries that see any of them, in the form in which it is used.
 struct alignas(16) Item {
-  int b, hk, key0;
-  int steps;    // 0: none (the sums only decay), -1: nothing to do
-  int prefix, n;  // cached and new tokens of the sequence
-  int q_begin;  // queries that count and see a key of the item: [q_begin, n)
-  int row;      // b, hk as one index
-  __device__ __forceinline__ int total() const { return prefix + n; }
+  int64_t sums_at, table_at, lse_at;  // of its first key's sum, its first page's entry, its first query's lse
+  int steps;    // of columns; 0: none (the sums only decay), -1: nothing to do
+  int keys;     // up to the end of the sequence (256 or more: all)
+  int queries;  // that count and see a key of the item
+  int diag;     // key t of the item is seen from query t + diag of them on
+  int b, hk, query0;
 };
-static_assert(sizeof(Item) == 32, "item list");
+static_assert(sizeof(Item) == 64, "item list");
 
 __device__ __forceinline__ Item make_item(const ChunkWeightsArgs& a, int index, int qpt_log2) {
-  const int rows = a.batch * a.n_kv_heads;
+  const int rows = a.batch * a.n_kv_heads, row = index % rows, key0 = index / rows * CK;
   Item it{};
-  it.row = index % rows;
-  it.b = it.row / a.n_kv_heads;
-  it.hk = it.row % a.n_kv_heads;
-  it.key0 = index / rows * CK;
+  it.b = row / a.n_kv_heads;
+  it.hk = row % a.n_kv_heads;
   it.steps = -1;
   const int64_t prefix = __ldg(a.prefix_lens + it.b);
   const int64_t n = a.chunk_lens ? __ldg(a.chunk_lens + it.b) : a.chunk_len;
   if (prefix < 0 || n < 0 || n > a.chunk_len || prefix + n > (int64_t)a.max_blocks * a.page_size) {
-    if (it.hk == 0 && it.key0 == 0) set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
+    if (it.hk == 0 && key0 == 0) set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
     return it;
   }
-  it.prefix = (int)prefix;
-  it.n = (int)n;
-  if (it.key0 >= it.total()) return it;
-  const int first = a.window > 0 && a.window < it.n ? it.n - a.window : 0;
-  it.q_begin = max(first, it.key0 - it.prefix);
-  it.steps = it.n > it.q_begin ? (it.n - it.q_begin + (1 << qpt_log2) - 1) >> qpt_log2 : 0;
+  it.keys = (int)(prefix + n) - key0;
+  if (it.keys <= 0) return it;
+  const int first = a.window > 0 && a.window < n ? (int)n - a.window : 0;
+  it.query0 = max(first, key0 - (int)prefix);
+  it.queries = max(0, (int)n - it.query0);
+  it.diag = key0 - (int)prefix - it.query0;
+  it.steps = (it.queries + (1 << qpt_log2) - 1) >> qpt_log2;
+  it.sums_at = (int64_t)row * (a.max_blocks * a.page_size) + key0;
+  it.table_at = (int64_t)it.b * a.max_blocks + key0 / 16;
+  it.lse_at = (int64_t)row * (a.n_qo_heads / a.n_kv_heads) * a.chunk_len + it.query0;
   return it;
 }
 
@@ -197,12 +199,11 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   };
   auto my_key = [&](const Item& it, int t) {
     Mine m{};
-    const int key = it.key0 + t;
-    m.live = key < it.total();
+    m.live = t < it.keys;
     if (m.live) {
-      m.at = (int64_t)it.row * (a.max_blocks * a.page_size) + key;
+      m.at = it.sums_at + t;
       m.before = a.sums_in[m.at];
-      m.page = __ldg(a.block_table + (int64_t)it.b * a.max_blocks + key / 16);
+      m.page = __ldg(a.block_table + it.table_at + t / 16);
     }
     return m;
   };
@@ -227,10 +228,7 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       // first page again (their keys are not written), a bad entry page 0 (its keys become NaN).
       // The next item's entries are asked for before this item's copies wait for room.
       auto entry = [&](const Item& it) {
-        const int pages = min(CK / 16, (it.total() - it.key0 + 15) / 16);
-        return lane < 16 && it.steps > 0
-                   ? __ldg(a.block_table + (int64_t)it.b * a.max_blocks + it.key0 / 16 + (lane < pages ? lane : 0))
-                   : 0;
+        return lane < 16 && it.steps > 0 ? __ldg(a.block_table + it.table_at + (16 * lane < it.keys ? lane : 0)) : 0;
       };
       Item next{};
       int next_phys = 0;
@@ -284,8 +282,8 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           if (elect_one()) {
             mbar_arrive_expect_tx(bar(C_QF + qs), QSTG);
             const uint32_t dst = sb + SM_Q + qs * QSTG;
-            tma_load_4d(dst, &mq, 0, it.hk * G, it.q_begin + s * qpt, it.b, bar(C_QF + qs));
-            tma_load_4d(dst + HALF, &mq, 64, it.hk * G, it.q_begin + s * qpt, it.b, bar(C_QF + qs));
+            tma_load_4d(dst, &mq, 0, it.hk * G, it.query0 + s * qpt, it.b, bar(C_QF + qs));
+            tma_load_4d(dst + HALF, &mq, 64, it.hk * G, it.query0 + s * qpt, it.b, bar(C_QF + qs));
           }
           __syncwarp();
         }
@@ -356,12 +354,12 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     const uint32_t src = tmem + lane_addr + (2 * tile + half) * CN;
     auto lse_of = [&](const Item& it, int s, float (&v)[LC]) {
       if (s >= it.steps) return;
-      const int q0 = it.q_begin + (s << qpt_log2);
-      const float* rows = a.lse + (int64_t)(it.row << g_log2) * a.chunk_len + q0;
+      const float* first = a.lse + it.lse_at + (s << qpt_log2);
+      const int left = it.queries - (s << qpt_log2);
 #pragma unroll
       for (int k = 0; k < LC; ++k) {
         const int col = 32 * k + lane, query = col >> g_log2;
-        v[k] = q0 + query < it.n ? __ldg(rows + (int64_t)(col & (G - 1)) * a.chunk_len + query) : 0.0f;
+        v[k] = query < left ? __ldg(first + (int64_t)(col & (G - 1)) * a.chunk_len + query) : 0.0f;
       }
     };
     // look() goes on to the next item that these warps have a part in, and asks for its old sums,
@@ -401,7 +399,6 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 #pragma unroll
       for (int k = 0; k < LC; ++k) v[k] = ahead[k];
       look();
-      const int key = now.key0 + t;
       float total = 0.0f;
       const int mine_first = (int)((half ^ qc) & 1);  // of the item's steps, this half takes every other one
       for (int k0 = mine_first; ok && k0 < n_steps; k0 += 2) {
@@ -413,10 +410,9 @@ chunk_weights_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         ok = warp_wait(bar(C_SF + 2 * tile + half), ((qc + k0) / 2) & 1);
         if (!ok) break;
         tc_fence_after();
-        const int q0 = now.q_begin + s * qpt;
         // columns [lo, hi) count: the causal bound and the end of the chunk
-        const int lo = (key - now.prefix - q0) * G, hi = min(CN, (now.n - q0) * G);
-        const bool whole = __all_sync(0xffffffffu, lo <= 0) && hi == CN;
+        const int lo = max(now.diag + t - s * qpt, 0) * G, hi = min(qpt, now.queries - s * qpt) * G;
+        const bool whole = __all_sync(0xffffffffu, lo == 0) && hi == CN;
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < CN / 32; ++k) {

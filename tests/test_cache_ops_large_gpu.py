@@ -122,3 +122,26 @@ def test_a_stalled_decode_makes_its_sums_nan(b):
     w = oracle.key_weights(c.q[1:, None].double().numpy(), c.k_pages.nan_to_num(0).double().numpy(), c.block_table.numpy()[1:],
                            c.kv_lens.numpy()[1:] - 1, lse[1:, :, None].cpu().double().numpy(), c.scale)
     np.testing.assert_allclose(got[1, :, :40].cpu().numpy(), w[0, :, :40], rtol=1e-4)
+
+
+def test_chunk_weights_far_back(b):
+    """A key 2^24 and more tokens behind the query, with 128 heads on a KV head: the causal bound in columns is past
+    32 bits. All blocks are one of three pages, so the answer repeats."""
+    blocks, hq, scale = (1 << 21) + 8, 128, 128 ** -0.5
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kp = torch.randn(3, 1, 16, 128, device="cuda", generator=g, dtype=torch.bfloat16)
+    q = torch.randn(1, 2, hq, 128, device="cuda", generator=g, dtype=torch.bfloat16)
+    table = (torch.arange(blocks, device="cuda") % 3).to(torch.int32).view(1, blocks)
+    n = blocks * 16
+    lse = torch.full((1, hq, 2), 12.0, device="cuda")
+    sums = torch.zeros(1, 1, n, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pl = torch.tensor([n - 2], dtype=torch.int32, device="cuda")
+    got = b.chunk_weights(q, kp, table, pl, lse, sums, scale, err_flag=err)
+    assert int(err) == 0
+    w = (torch.einsum("qhd,ptd->qhpt", q[0].double(), kp[:, 0].double()) * scale - 12.0).exp().sum(1).reshape(2, 48)
+    want = (w[0] + w[1]).repeat(n // 48 + 1)[:n]
+    want[n - 1] = w[1][(n - 1) % 48]  # the last key is seen by the last query alone
+    top = scale * float(q.double().abs().amax() * kp.double().abs().sum(-1).amax())
+    bar = 2.0 ** -22 * (128 * top + 4 * (top + 12.0)) + 2.0 ** -20 + 2 * (hq + 8) * 2.0 ** -24 + 2.0 ** -23
+    assert float(((got[0, 0].double() - want).abs() / want).max()) <= bar
