@@ -401,24 +401,18 @@ def flat_gemm(x, w, out=None, err_flag=None, stream=None):
 
 # --------------------------------------------------------------------------- cache write
 
-_fast_need = _pycall.need
+_fast_need, _rows = _pycall.need, _pycall.rows
+_I32, _F32 = torch.int32, torch.float32
 
 
-def _token_rows(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
-    """Checks ``[B, C, H, D]`` whose head rows are contiguous per token; the token stride."""
-    step = _pycall.rows(t, dev, dtype, shape)
-    if step >= 0:
-        return step
+def _bad_token_rows(t: torch.Tensor, name: str, dev: int, dtype, shape):
+    """Says why ``_pycall.rows`` does not take ``t`` as ``[B, C, H, D]`` with one stride per token."""
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    B, C, H, D = shape
-    sb, sc, sh, sd = t.stride()
-    if (sd == 1 or D == 1) and (sh == D or H == 1) and (sb == C * sc or B == 1 or C == 1):
-        return sc if C > 1 else sb if B > 1 else H * D
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     raise ValueError(f"{name} must hold each token's heads contiguously at one stride per token, got {t.stride()}")
 
 
@@ -436,31 +430,32 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chu
         raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
     max_blocks = block_table.shape[1]
     dev, dtype, need = _device_of(q), q.dtype, _fast_need
-    qs = _token_rows(q, "q", dev, dtype, rows)
-    ks = _token_rows(k, "k", dev, dtype, (B, C, Hkv, D))
-    vs = _token_rows(v, "v", dev, dtype, (B, C, Hkv, D))
+    kv_rows = (B, C, Hkv, D)
+    q_at = _rows(q, dev, dtype, rows) or _bad_token_rows(q, "q", dev, dtype, rows)
+    k_at = _rows(k, dev, dtype, kv_rows) or _bad_token_rows(k, "k", dev, dtype, kv_rows)
+    v_at = _rows(v, dev, dtype, kv_rows) or _bad_token_rows(v, "v", dev, dtype, kv_rows)
     n_axes = 1
     if positions is not None:
         if positions.dim() == 3:
             n_axes = positions.shape[0]
-            positions = need(positions, "positions", dev, torch.int32, (n_axes, B, C))
+            positions = need(positions, "positions", dev, _I32, (n_axes, B, C))
         else:
-            positions = need(positions, "positions", dev, torch.int32, (B, C))
+            positions = need(positions, "positions", dev, _I32, (B, C))
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        inv_freq = need(inv_freq, "inv_freq", dev, torch.float32, (rot // 2,))
+        inv_freq = need(inv_freq, "inv_freq", dev, _F32, (rot // 2,))
     if out is None:
         out = torch.empty((B, C, Hq, D), dtype=dtype, device=q.device)
     st = _pycall.attn_qk_norm_rope_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+        q_at[0], k_at[0], v_at[0], q_at[1], k_at[1], v_at[1],
         None if q_norm is None else need(q_norm, "q_norm", dev, dtype, (D,)),
         None if k_norm is None else need(k_norm, "k_norm", dev, dtype, (D,)), float(eps), inv_freq, rot,
         1 if interleaved else 0, positions, n_axes,
-        None if pair_axis is None else need(pair_axis, "pair_axis", dev, torch.int32, (rot // 2,)),
-        need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
-        need(prefix_lens, "prefix_lens", dev, torch.int32, (B,)),
-        None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, torch.int32, (B,)),
+        None if pair_axis is None else need(pair_axis, "pair_axis", dev, _I32, (rot // 2,)),
+        need(block_table, "block_table", dev, _I32, (B, max_blocks)),
+        need(prefix_lens, "prefix_lens", dev, _I32, (B,)),
+        None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, _I32, (B,)),
         need(out, "out", dev, dtype, rows), need(k_pages, "k_pages", dev, dtype, None),
         need(v_pages, "v_pages", dev, dtype, k_pages.shape), B, C, max_blocks, num_pages, Hq, Hkv, D, P, _dt(q),
         _ptr(err_flag), _stream(stream, dev))
@@ -492,24 +487,24 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums,
     dev, dtype, need = _device_of(q), q.dtype, _fast_need
     q_ptr = need(q, "q", dev, None, None)
     sums = (B, Hkv, max_blocks * P)
-    in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, torch.float32, sums)
+    in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, _F32, sums)
     if sums_out is None:
         sums_out = weight_sums
     else:
-        out_ptr = need(sums_out, "sums_out", dev, torch.float32, sums)
+        out_ptr = need(sums_out, "sums_out", dev, _F32, sums)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, Hq), dtype=_F32, device=q.device)
     if workspace is None:
         workspace = alloc_workspace(decode_weights_workspace_size(B, max_blocks, Hq, Hkv, D, P, num_splits, _dt(q)),
                                     q.device)
     ws_ptr = None if workspace is None else need(workspace, "workspace", dev, None, None)
     st = _pycall.attn_decode_paged_weights(
         q_ptr, need(k_pages, "k_pages", dev, dtype, None), need(v_pages, "v_pages", dev, dtype, k_pages.shape),
-        need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
-        need(kv_lens, "kv_lens", dev, torch.int32, (B,)), need(out, "out", dev, dtype, (B, Hq, D)),
-        need(lse, "lse", dev, torch.float32, (B, Hq)), in_ptr, out_ptr, B, max_blocks, num_pages, Hq, Hkv, D, P,
+        need(block_table, "block_table", dev, _I32, (B, max_blocks)),
+        need(kv_lens, "kv_lens", dev, _I32, (B,)), need(out, "out", dev, dtype, (B, Hq, D)),
+        need(lse, "lse", dev, _F32, (B, Hq)), in_ptr, out_ptr, B, max_blocks, num_pages, Hq, Hkv, D, P,
         float(scale), float(decay), int(num_splits), _dt(q), ws_ptr, 0 if workspace is None else workspace.nbytes, _ptr(err_flag),
         _stream(stream, dev))
     _check(st, "attn_decode_paged_weights")
@@ -529,17 +524,17 @@ def chunk_weights(q, k_pages, block_table, prefix_lens, lse, weight_sums, scale,
     dev, dtype, need = _device_of(q), q.dtype, _fast_need
     q_ptr = need(q, "q", dev, None, None)
     sums = (B, Hkv, max_blocks * P)
-    in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, torch.float32, sums)
+    in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, _F32, sums)
     if sums_out is None:
         sums_out = weight_sums
     else:
-        out_ptr = need(sums_out, "sums_out", dev, torch.float32, sums)
+        out_ptr = need(sums_out, "sums_out", dev, _F32, sums)
     st = _pycall.attn_chunk_weights(
         q_ptr, need(k_pages, "k_pages", dev, dtype, None),
-        need(block_table, "block_table", dev, torch.int32, (B, max_blocks)),
-        need(prefix_lens, "prefix_lens", dev, torch.int32, (B,)),
-        None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, torch.int32, (B,)),
-        need(lse, "lse", dev, torch.float32, (B, Hq, C)), in_ptr, out_ptr, B, C, int(window), max_blocks, num_pages, Hq,
+        need(block_table, "block_table", dev, _I32, (B, max_blocks)),
+        need(prefix_lens, "prefix_lens", dev, _I32, (B,)),
+        None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, _I32, (B,)),
+        need(lse, "lse", dev, _F32, (B, Hq, C)), in_ptr, out_ptr, B, C, int(window), max_blocks, num_pages, Hq,
         Hkv, D, P, float(scale), float(decay), _dt(q), _ptr(err_flag), _stream(stream, dev))
     _check(st, "attn_chunk_weights")
     return sums_out
@@ -553,21 +548,20 @@ def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_t
     B, max_blocks = block_table.shape
     new_blocks = new_block_table.shape[1]
     dev, need, budget = _device_of(k_pages), _fast_need, int(budget)
-    i32, f32 = torch.int32, torch.float32
     k_ptr = need(k_pages, "k_pages", dev, None, None)
     if kept is None:
-        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=i32, device=k_pages.device)
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=_I32, device=k_pages.device)
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=i32, device=k_pages.device)
+        new_lens = torch.empty((B,), dtype=_I32, device=k_pages.device)
     if new_sums is None:
-        new_sums = torch.empty((B, Hkv, new_blocks * P), dtype=f32, device=k_pages.device)
+        new_sums = torch.empty((B, Hkv, new_blocks * P), dtype=_F32, device=k_pages.device)
     st = _pycall.attn_cache_evict(
         k_ptr, need(v_pages, "v_pages", dev, k_pages.dtype, k_pages.shape),
-        need(block_table, "block_table", dev, i32, None), need(kv_lens, "kv_lens", dev, i32, (B,)),
-        need(weight_sums, "weight_sums", dev, f32, (B, Hkv, max_blocks * P)),
-        need(new_block_table, "new_block_table", dev, i32, (B, new_blocks)),
-        need(kept, "kept", dev, i32, (B, Hkv, max(budget, 0))), need(new_lens, "new_lens", dev, i32, (B,)),
-        need(new_sums, "new_sums", dev, f32, (B, Hkv, new_blocks * P)), B, max_blocks, new_blocks, num_pages, Hkv, D, P,
+        need(block_table, "block_table", dev, _I32, None), need(kv_lens, "kv_lens", dev, _I32, (B,)),
+        need(weight_sums, "weight_sums", dev, _F32, (B, Hkv, max_blocks * P)),
+        need(new_block_table, "new_block_table", dev, _I32, (B, new_blocks)),
+        need(kept, "kept", dev, _I32, (B, Hkv, max(budget, 0))), need(new_lens, "new_lens", dev, _I32, (B,)),
+        need(new_sums, "new_sums", dev, _F32, (B, Hkv, new_blocks * P)), B, max_blocks, new_blocks, num_pages, Hkv, D, P,
         budget, int(n_sink), int(n_recent), _dt(k_pages), _ptr(err_flag), _stream(stream, dev))
     _check(st, "attn_cache_evict")
     return kept, new_lens, new_sums

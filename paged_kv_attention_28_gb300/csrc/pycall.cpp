@@ -96,25 +96,24 @@ static PyObject* need(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyObject_CallMethodNoArgs(t, s_data_ptr);
 }
 
-// rows(tensor, device, dtype, (B, C, H, D)) -> elements from one token to the next, where each token's
-// heads lie contiguously at one distance per token; -1 where that does not hold.
+// rows(tensor, device, dtype, (B, C, H, D)) -> (address of its data, elements from one token to the next),
+// where each token's heads lie contiguously at one distance per token; None where that does not hold.
 static PyObject* rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (n != 4) return PyErr_Format(PyExc_TypeError, "rows() takes 4 arguments, got %zd", n);
   const long dev = PyLong_AsLong(a[1]);
   if (dev == -1 && PyErr_Occurred()) return NULL;
-  int64_t step = -1;
   try {
     const at::Tensor* x = look(a[0], dev, a[2], a[3]);
     if (x && x->dim() == 4) {
       const int64_t B = x->size(0), C = x->size(1), H = x->size(2), D = x->size(3);
       const int64_t sb = x->stride(0), sc = x->stride(1);
       if ((x->stride(3) == 1 || D == 1) && (x->stride(2) == D || H == 1) && (sb == C * sc || B == 1 || C == 1))
-        step = C > 1 ? sc : B > 1 ? sb : H * D;
+        return Py_BuildValue("(NL)", PyLong_FromVoidPtr(x->data_ptr()), (long long)(C > 1 ? sc : B > 1 ? sb : H * D));
     }
   } catch (const std::exception&) {
   }
-  return PyLong_FromLongLong(step);
+  Py_RETURN_NONE;
 }
 
 // Raw arguments: addresses (int or None), integers and floats, as many as the call takes.

@@ -204,11 +204,12 @@ def test_native_checks_of_real_tensors():
         with pytest.raises(ValueError):
             _pycall.need(t, "x", dev, d, s)
     fused = torch.zeros(3, 5, 24, 16, dtype=torch.bfloat16, device="cuda")
-    assert _pycall.rows(x, 0, bf, dims) == 128
-    assert _pycall.rows(fused[:, :, 8:16], 0, bf, dims) == 24 * 16
-    assert _pycall.rows(fused[:, :1, 8:16], 0, bf, (3, 1, 8, 16)) == 5 * 24 * 16
-    assert _pycall.rows(fused[:1, :1, 8:16], 0, bf, (1, 1, 8, 16)) == 8 * 16
+    assert _pycall.rows(x, 0, bf, dims)[1] == 128
+    assert _pycall.rows(fused[:, :, 8:16], 0, bf, dims)[1] == 24 * 16
+    assert _pycall.rows(fused[:, :1, 8:16], 0, bf, (3, 1, 8, 16))[1] == 5 * 24 * 16
+    assert _pycall.rows(fused[:1, :1, 8:16], 0, bf, (1, 1, 8, 16))[1] == 8 * 16
     for t, s in ((fused[:, :4, 8:16], (3, 4, 8, 16)), (fused[:, :, 8:16:2], (3, 5, 4, 16)), (fused[..., :8], (3, 5, 24, 8)),
                  (x, (3, 5, 16, 8))):
-        assert _pycall.rows(t, 0, bf, s) == -1
-    assert _pycall.rows(x, 1, bf, dims) == -1 and _pycall.rows(x, 0, torch.float16, dims) == -1
+        assert _pycall.rows(t, 0, bf, s) is None
+    assert _pycall.rows(x, 1, bf, dims) is None and _pycall.rows(x, 0, torch.float16, dims) is None
+    assert _pycall.rows(fused[:, :, 8:16], 0, bf, dims)[0] == fused[:, :, 8:16].data_ptr()

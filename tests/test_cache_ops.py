@@ -245,7 +245,7 @@ def test_need_checks_a_tensor(b):
     with pytest.raises(ValueError, match="contiguous"):
         _pycall.need(T, "t", 0, None, None)
     for x in (T, torch.zeros(1, 2, 3, 4), torch.zeros(1, 2, 3, 4, device="meta"), None):
-        assert _pycall.rows(x, 0, torch.float32, (1, 2, 3, 4)) == -1
+        assert _pycall.rows(x, 0, torch.float32, (1, 2, 3, 4)) is None
     with pytest.raises(ValueError, match="t must be a CUDA tensor"):
         _pycall.need(torch.zeros(2, device="meta"), "t", 0, None, None)
     with pytest.raises(AttributeError):
