@@ -9,19 +9,25 @@
 // thread owns one key, i.e. one TMEM lane, so a key's sum over the columns never leaves its
 // thread: no reduction across threads, and a fixed order of additions.
 //
-// Bound: per 256 x 128 step the special-function unit needs 2048 clocks at 16 exponentials a clock
-// and SM, the two products 1024, which read 128 bytes a clock of shared memory all that time, and the
-// columns' log-sum-exps are read from there too. Measured 1090 ns (about 2070 clocks) a step: the
-// prompt chunk of 2048 queries over 2 x 3-4k keys, 32 heads on 8, takes 92 us. Tried and not kept: a
-// share of the exponentials as polynomials on the FMA units (12 % slower for each eighth: the issue
-// slots are not free), eight exponential warps for sixteen (14 % slower), one warp issuing the
-// products of both tiles (the tensor cores idle while it waits), two-wide fp32 arithmetic.
+// Bound: issue slots. A 256 x 128 step is 32768 exponentials, 1024 clocks of an SM's special-function
+// units at 32 a clock, 8.4 MFLOP, about as long on the tensor cores, and three more instructions an
+// exponential for the issue slots. A prompt chunk of 2048 queries over 2 x 3-4k keys, 32 heads on 8, takes
+// 85.5 us (1.0 PFLOP/s); of the clocks in which an SM works, 68 % issue, 52 % have the
+// special-function and 52 % the tensor pipe busy, and the SMs work 80 % of the time: about 230
+// unequal items do not divide by 152. Tried and not kept: a share of the exponentials as
+// polynomials on the FMA units (12 % slower for each eighth: the issue slots are not free), eight
+// exponential warps for sixteen (14 % slower), one warp issuing the products of both tiles (the tensor
+// cores idle while it waits), two-wide fp32 arithmetic, tensor memory read in double-buffered
+// halves (10 % slower: spills), pages loaded by two warps (no gain).
 // With a window of few queries an item is a single step, and what bounds it is the chain of
-// barriers, loads and address arithmetic around the step, about 2.8 us of a CTA an item.
+// barriers, loads and address arithmetic around the step, about 1.8 us of a CTA an item (32 queries
+// over 4 x 5k keys: 13.7 us, 3.5 TB/s).
 //
 // A persistent CTA per SM takes items (sequence, KV head, 256 keys) in an order that pairs long and
 // short ones: key tiles slowest (early keys are seen by the most queries), and every other round
-// of the CTAs backwards (135 to 108 us against a plain stride). With fewer items than half the SMs
+// of the CTAs backwards (135 to 108 us against a plain stride). All its threads work its list of
+// items out at the start, for every warp to read (16.3 to 13.7 us for the window: each warp working
+// them out by itself took longer than its step). With fewer items than half the SMs
 // an item's steps are shared by a cluster of 2 to 8 CTAs, whose partial sums are added in rank
 // order through distributed shared memory.
 // Warps: 0 and 2 TMA producers (a ring of four K tiles, page by page, and one of two Q tiles), 1

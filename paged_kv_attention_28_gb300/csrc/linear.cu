@@ -29,7 +29,7 @@ namespace {
 
 constexpr int LBK = 64;              // K per block of a stage: one 128-byte swizzled row
 constexpr int BLK = 128 * LBK * 2;   // a CTA's tokens (or most features) of a block
-constexpr int LTHREADS = 256;
+constexpr int LTHREADS = 384;      // TMA, MMA, two idle warps, eight for the epilogue
 constexpr int PANEL = 16;  // token tiles walked before the next feature tile: their x stays in L2
 
 struct LinArgs {
@@ -55,24 +55,25 @@ __device__ __forceinline__ void tile_at(int i, int tiles_m, int tiles_n, int& tm
   tn = r / rows;
 }
 
-// N consecutive features of one token, those from `end` on not stored.
-template <int N>
-__device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[N], int row, int col, int end) {
-  const __nv_bfloat16* bias = a.ep.bias;
+// 32 features of one token, those from `end` on not stored. `bias` holds theirs (0 from `end` on); `res`
+// the residual's, where they are all stored and its rows are aligned.
+__device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[32], const float* bias, const uint4 (&res)[4], int row,
+                                           int col, int end) {
+  constexpr int N = 32;
   const int64_t at = (int64_t)row * a.n + col;
-  if (a.vec && col + N <= end) {
-    if (bias) {
+  if (a.ep.bias) {
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(bias + col + i));
-        v[i] += b.x, v[i + 1] += b.y;
-      }
+    for (int i = 0; i < N; i += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(bias + i);
+      v[i] += b.x, v[i + 1] += b.y, v[i + 2] += b.z, v[i + 3] += b.w;
     }
-    activate_all(v, a.ep.activation);
+  }
+  activate_all(v, a.ep.activation);
+  if (a.vec && col + N <= end) {
     if (a.ep.residual) {
 #pragma unroll
       for (int i = 0; i < N; i += 8) {
-        const uint4 r = *reinterpret_cast<const uint4*>(a.ep.residual + at + i);
+        const uint4 r = res[i / 8];
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -97,12 +98,6 @@ __device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[N], int 
         *reinterpret_cast<uint4*>(a.y + at + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
   } else {
-    if (bias) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (col + i < end) v[i] += __bfloat162float(bias[col + i]);
-    }
-    activate_all(v, a.ep.activation);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (col + i < end) {
@@ -121,7 +116,8 @@ template <int SUB>
 struct LinCfg {
   static constexpr int PST = 6 / SUB, STG = SUB * BLK;  // stages; bytes of one operand's stage
   static constexpr int SM_B = PST * STG, SM_BAR = 2 * PST * STG, NBAR = 2 * PST + 5, SM_MISC = SM_BAR + NBAR * 8,
-                       SMEM = SM_MISC + 16 + 1024;
+                       SM_BIAS = (SM_MISC + 16 + 15) / 16 * 16,  // [8 warps][4 runs][32]
+                       SMEM = SM_BIAS + 8 * 4 * 32 * 4 + 1024;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -194,7 +190,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(acc_full + 8 * s, 1);
-      mbar_init(acc_empty + 8 * s, 8);
+      mbar_init(acc_empty + 8 * s, 16);
     }
     mbar_init(drain, 1);
     misc->abort_ = 0;
@@ -299,20 +295,58 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     if (!warp_wait(drain, 0)) give_up();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    const int wq = warp & 3;
+    // Two warps for each quarter of the tokens, which take the runs of 32 features in turn. The
+    // epilogue of a short product is a chain of loads, so they are asked for early: the bias of a
+    // tile in the tile before (through shared memory), the residual's lines come to the L2 in the tile
+    // before and to registers two runs ahead (2611 x 11008 x 256: 77 to TIME us).
+    const int wq = warp & 3, group = (warp - 4) >> 2;
+    float* bias_s = reinterpret_cast<float*>(smem + C::SM_BIAS) + (warp - 4) * 128;
+    float bias_next[4] = {};
+    auto ask_bias = [&](int col0, int end) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int col = col0 + 32 * group + 64 * k + lane;
+        bias_next[k] = a.ep.bias && col < end ? __bfloat162float(a.ep.bias[col]) : 0.0f;
+      }
+    };
     uint32_t t = 0;
     bool ok = true;
+    int tm = 0, tn = 0;
+    if (pair < a.tiles) {
+      tile_at(pair, a.tiles_m, tiles_n, tm, tn);
+      ask_bias(tn * bn, min(a.n, (tn + 1) * bn));
+    }
     for (int i = pair; i < a.tiles; i += pairs, ++t) {
-      int tm, tn;
-      tile_at(i, a.tiles_m, tiles_n, tm, tn);
       const uint32_t buf = t & 1;
+      const int row = tm * PBM + rank * 128 + wq * 32 + lane;
+      const int end = min(a.n, (tn + 1) * bn), col0 = tn * bn;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) bias_s[32 * k + lane] = bias_next[k];
+      if (i + pairs < a.tiles) {
+        tile_at(i + pairs, a.tiles_m, tiles_n, tm, tn);
+        const int next0 = tn * bn, next_end = min(a.n, next0 + bn), next_row = tm * PBM + rank * 128 + wq * 32 + lane;
+        ask_bias(next0, next_end);
+        if (a.ep.residual && next_row < a.m) {
+          for (int col = next0 + 64 * group; col < next_end; col += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.ep.residual + (int64_t)next_row * a.n + col));
+        }
+      }
+      __syncwarp();  // the bias is in
+      const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + buf * 256;
+      const __nv_bfloat16* res_row = a.ep.residual && a.vec && row < a.m ? a.ep.residual + (int64_t)row * a.n + col0 : nullptr;
+      auto ask = [&](uint4 (&r)[4], int cc) {
+        if (res_row && cc < bn && col0 + cc + 32 <= end) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = *reinterpret_cast<const uint4*>(res_row + cc + 8 * k);
+        }
+      };
+      uint4 res[4] = {}, next_res[4] = {};
+      ask(res, 32 * group);
+      ask(next_res, 32 * group + 64);
       if (ok && !warp_wait(acc_full + 8 * buf, (t / 2) & 1)) ok = false;
       tc_fence_after();
-      const int row = tm * PBM + rank * 128 + wq * 32 + lane;
-      const int end = min(a.n, (tn + 1) * bn);
-      const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + buf * 256;
 #pragma unroll 1
-      for (int cc = 0; cc + 32 <= bn; cc += 32) {
+      for (int cc = 32 * group; cc < bn; cc += 64) {
         uint32_t r[32];
         if (ok) {
           tmem_ld32(src + cc, r);
@@ -321,7 +355,10 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
         float v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = ok ? __uint_as_float(r[k]) : NAN;
-        if (row < a.m && tn * bn + cc < end) finish_row(a, v, row, tn * bn + cc, end);
+        if (row < a.m && col0 + cc < end) finish_row(a, v, bias_s + cc / 64 * 32, res, row, col0 + cc, end);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) res[k] = next_res[k];
+        ask(next_res, cc + 128);
         __syncwarp();
       }
       tc_fence_before();
@@ -394,8 +431,7 @@ int launch_linear(const LinearArgs& p, cudaStream_t stream) {
   const int64_t tiles = tm * (((int64_t)p.n + bn - 1) / bn);
   if (tiles > 0x7fffffffL) return PKV_ERR_UNSUPPORTED;
   const uintptr_t rows = reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.residual);
-  const bool bias_pairs = (reinterpret_cast<uintptr_t>(p.bias) & 3) == 0;
-  const int vec = !bias_pairs ? 0 : p.n % 16 == 0 && rows % 32 == 0 ? 32 : p.n % 8 == 0 && rows % 16 == 0 ? 16 : 0;
+  const int vec = p.n % 16 == 0 && rows % 32 == 0 ? 32 : p.n % 8 == 0 && rows % 16 == 0 ? 16 : 0;
   const int block = bn >= kWide ? LBK : 2 * LBK;
   const LinArgs a{static_cast<__nv_bfloat16*>(p.y),
                   Epilogue{static_cast<const __nv_bfloat16*>(p.bias), static_cast<const __nv_bfloat16*>(p.residual),
