@@ -22,7 +22,11 @@ struct Epilogue {
 // erff is off by 2 units in the last place of 1, i.e. 2^-23 |y| here.
 template <int ACT>
 __device__ __forceinline__ float activate(float y) {
-  if constexpr (ACT == PKV_ACT_RELU) return y < 0.0f ? 0.0f : y;  // NaN stays
+  if constexpr (ACT == PKV_ACT_RELU) {  // NaN stays
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(y));
+    return r;
+  }
   if constexpr (ACT == PKV_ACT_GELU) return 0.5f * y * (1.0f + erff(y * 0.70710678118654752f));
   if constexpr (ACT == PKV_ACT_GELU_TANH) {
     const float t = y * fmaf(y * y, -2.0f * 1.4426950408889634f * 0.7978845608028654f * 0.044715f,

@@ -5,12 +5,19 @@
 // 256 tokens x BN features per pair. One tcgen05 product spans both SMs of the pair: each holds its
 // 128 tokens and half of the features, so that a CTA reads half the weights a single one would, and
 // the fp32 accumulators of its tokens. Operands come by TMA through a ring of six 64-column blocks;
-// the accumulator is double-buffered, so four epilogue warps read one tile out of tensor memory,
+// the accumulator is double-buffered, so eight epilogue warps read one tile out of tensor memory,
 // apply bias, activation and residual in fp32 and store it (one rounding) while the next tile's
 // products run.
 //
-// Bound: the tensor cores, 2 m n k operations; for few tokens the weights' bytes. BN is the multiple
-// of 32 for which the rounds of tiles over the pairs take least (choose_width).
+// Bound: the tensor cores, 2 m n k operations; for few tokens the weights' bytes. 4096 x 11008 x 4096 with
+// bias and gelu takes 195 us in a burst (1.9 PFLOP/s, the rate of the library's plain product; the tensor
+// pipe is busy 91 % of the time) and 228 us under the power limit. BN is the multiple of 32 for which the
+// rounds of tiles over the pairs take least (choose_width); what is lost is the last round: 1024 x 4096
+// x 4096 takes 24 us where its products are 18. A short product is bound by its epilogue, whose loads
+// are a chain: 2611 x 11008 x 256 takes 28 us, 50 with a residual (46 and 77 with four warps that ask for
+// everything when they need it), of which the products with their operands from the L2 are 17. Not
+// kept: sixteen warps (no faster, small products 3 % slower), y through shared memory and TMA (the same
+// time where rows are aligned to 32 bytes).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -157,8 +164,10 @@ __device__ __forceinline__ void commit_pair(uint32_t mbar) {
       "h"((unsigned short)3)
       : "memory");
 }
+// Arrives on a barrier of the pair's first CTA. Relaxed: what it announces is that reads of tensor memory
+// are over, which tcgen05.wait::ld has seen to; a release would wait for the tile's stores as well.
 __device__ __forceinline__ void arrive_remote(uint32_t mbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
 
 // A cluster of two CTAs per tile of 256 tokens x bn features. The first CTA's MMA warp issues the
@@ -298,7 +307,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     // Two warps for each quarter of the tokens, which take the runs of 32 features in turn. The
     // epilogue of a short product is a chain of loads, so they are asked for early: the bias of a
     // tile in the tile before (through shared memory), the residual's lines come to the L2 in the tile
-    // before and to registers two runs ahead (2611 x 11008 x 256: 77 to TIME us).
+    // before and to registers two runs ahead.
     const int wq = warp & 3, group = (warp - 4) >> 2;
     float* bias_s = reinterpret_cast<float*>(smem + C::SM_BIAS) + (warp - 4) * 128;
     float bias_next[4] = {};
