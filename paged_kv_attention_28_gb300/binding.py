@@ -1,7 +1,7 @@
 """ctypes binding to ``libpkvattn.so``: the C ABI declared in ``include/pkv_attn.h``.
 
 This layer only marshals arguments, through ctypes or, for the operators whose smallest calls
-take less time than that, through the CPython module ``_pycall``. It turns torch CUDA tensors into device
+take less time than that, through the CPython module ``_pycall`` (csrc/pycall.cpp). It turns torch CUDA tensors into device
 pointers, checks shapes and dtypes on the host, and passes the current CUDA
 stream. Every step of the computation runs in the library's kernels. If the
 library is missing, importing this module raises; nothing falls back to
@@ -136,36 +136,16 @@ def _dt(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-# Small calls are bound by this file's host time, so the helpers hand ctypes plain integers and
-# decide the common case in one expression.
-
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-# The raw handle of a device's current stream, without building a torch.cuda.Stream (2 us).
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-def _stream(stream=None, device=None):
-    """The handle of ``stream``, or of the current one (of ``device``, the current device)."""
-    if stream is not None:
-        return stream.cuda_stream
-    if _current_raw_stream is not None:
-        return _current_raw_stream(torch.cuda.current_device() if device is None else device)
-    return torch.cuda.current_stream().cuda_stream
-
-
-def _device_of(t: torch.Tensor) -> int:
-    """The current device, where every tensor of a call has to be (-2 for a host tensor: no device)."""
-    return _current_device() if t.is_cuda else -2
+def _stream(stream=None):
+    s = torch.cuda.current_stream() if stream is None else stream
+    return ctypes.c_void_p(s.cuda_stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
-    if (t.is_cuda and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
-            and t.is_contiguous()):
-        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -401,21 +381,6 @@ def flat_gemm(x, w, out=None, err_flag=None, stream=None):
 
 # --------------------------------------------------------------------------- cache write
 
-_fast_need, _rows = _pycall.need, _pycall.rows
-_I32, _F32 = torch.int32, torch.float32
-
-
-def _bad_token_rows(t: torch.Tensor, name: str, dev: int, dtype, shape):
-    """Says why ``_pycall.rows`` does not take ``t`` as ``[B, C, H, D]`` with one stride per token."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must hold each token's heads contiguously at one stride per token, got {t.stride()}")
-
-
 def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chunk_lens=None, positions=None,
                         inv_freq=None, pair_axis=None, q_norm=None, k_norm=None, eps=1e-6, interleaved=False,
                         out=None, err_flag=None, stream=None):
@@ -424,42 +389,11 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chu
     ``q`` ``[B, C, Hq, D]`` and ``k``, ``v`` ``[B, C, Hkv, D]`` may be slices of one fused
     projection; ``positions`` ``[n_axes, B, C]`` (or ``[B, C]`` for one axis). Returns the
     rotated queries ``[B, C, Hq, D]``."""
-    B, C, Hq, D = rows = q.shape
-    num_pages, Hkv, P, D2 = k_pages.shape
-    if D2 != D:
-        raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
-    max_blocks = block_table.shape[1]
-    dev, dtype, need = _device_of(q), q.dtype, _fast_need
-    kv_rows = (B, C, Hkv, D)
-    q_at = _rows(q, dev, dtype, rows) or _bad_token_rows(q, "q", dev, dtype, rows)
-    k_at = _rows(k, dev, dtype, kv_rows) or _bad_token_rows(k, "k", dev, dtype, kv_rows)
-    v_at = _rows(v, dev, dtype, kv_rows) or _bad_token_rows(v, "v", dev, dtype, kv_rows)
-    n_axes = 1
-    if positions is not None:
-        if positions.dim() == 3:
-            n_axes = positions.shape[0]
-            positions = need(positions, "positions", dev, _I32, (n_axes, B, C))
-        else:
-            positions = need(positions, "positions", dev, _I32, (B, C))
-    rot = 0
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        inv_freq = need(inv_freq, "inv_freq", dev, _F32, (rot // 2,))
     if out is None:
-        out = torch.empty((B, C, Hq, D), dtype=dtype, device=q.device)
-    st = _pycall.attn_qk_norm_rope_append(
-        q_at[0], k_at[0], v_at[0], q_at[1], k_at[1], v_at[1],
-        None if q_norm is None else need(q_norm, "q_norm", dev, dtype, (D,)),
-        None if k_norm is None else need(k_norm, "k_norm", dev, dtype, (D,)), float(eps), inv_freq, rot,
-        1 if interleaved else 0, positions, n_axes,
-        None if pair_axis is None else need(pair_axis, "pair_axis", dev, _I32, (rot // 2,)),
-        need(block_table, "block_table", dev, _I32, (B, max_blocks)),
-        need(prefix_lens, "prefix_lens", dev, _I32, (B,)),
-        None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, _I32, (B,)),
-        need(out, "out", dev, dtype, rows), need(k_pages, "k_pages", dev, dtype, None),
-        need(v_pages, "v_pages", dev, dtype, k_pages.shape), B, C, max_blocks, num_pages, Hq, Hkv, D, P, _dt(q),
-        _ptr(err_flag), _stream(stream, dev))
-    _check(st, "attn_qk_norm_rope_append")
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _check(_pycall.qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chunk_lens, positions, inv_freq,
+                                       pair_axis, q_norm, k_norm, eps, interleaved, out, err_flag, stream),
+           "attn_qk_norm_rope_append")
     return out
 
 
@@ -479,35 +413,18 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums,
     """Paged decode that adds each key's attention weight to ``weight_sums``
     ``[B, Hkv, max_blocks * page_size]`` (in place, or into ``sums_out``), through
     ``attn_decode_paged_weights``. Returns ``(out, lse, sums)``."""
-    B, Hq, D = q.shape
-    num_pages, Hkv, P, D2 = k_pages.shape
-    if D2 != D:
-        raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
-    max_blocks = block_table.shape[1]
-    dev, dtype, need = _device_of(q), q.dtype, _fast_need
-    q_ptr = need(q, "q", dev, None, None)
-    sums = (B, Hkv, max_blocks * P)
-    in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, _F32, sums)
-    if sums_out is None:
-        sums_out = weight_sums
-    else:
-        out_ptr = need(sums_out, "sums_out", dev, _F32, sums)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=_F32, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = alloc_workspace(decode_weights_workspace_size(B, max_blocks, Hq, Hkv, D, P, num_splits, _dt(q)),
-                                    q.device)
-    ws_ptr = None if workspace is None else need(workspace, "workspace", dev, None, None)
-    st = _pycall.attn_decode_paged_weights(
-        q_ptr, need(k_pages, "k_pages", dev, dtype, None), need(v_pages, "v_pages", dev, dtype, k_pages.shape),
-        need(block_table, "block_table", dev, _I32, (B, max_blocks)),
-        need(kv_lens, "kv_lens", dev, _I32, (B,)), need(out, "out", dev, dtype, (B, Hq, D)),
-        need(lse, "lse", dev, _F32, (B, Hq)), in_ptr, out_ptr, B, max_blocks, num_pages, Hq, Hkv, D, P,
-        float(scale), float(decay), int(num_splits), _dt(q), ws_ptr, 0 if workspace is None else workspace.nbytes, _ptr(err_flag),
-        _stream(stream, dev))
-    _check(st, "attn_decode_paged_weights")
+        B, Hq, D = q.shape
+        workspace = alloc_workspace(decode_weights_workspace_size(B, block_table.shape[1], Hq, k_pages.shape[1], D,
+                                                                  k_pages.shape[2], num_splits, _dt(q)), q.device)
+    if sums_out is None:
+        sums_out = weight_sums
+    _check(_pycall.decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums, sums_out, scale, decay,
+                                        num_splits, out, lse, workspace, err_flag, stream), "attn_decode_paged_weights")
     return out, lse, sums_out
 
 
@@ -516,27 +433,10 @@ def chunk_weights(q, k_pages, block_table, prefix_lens, lse, weight_sums, scale,
     """Adds the attention weight that every key receives from a chunk's queries (the last
     ``window`` of them; 0: all) to ``weight_sums`` (in place, or into ``sums_out``), through
     ``attn_chunk_weights``. ``lse`` ``[B, Hq, C]`` is ``prefill_paged_chunk``'s. Returns the sums."""
-    B, C, Hq, D = q.shape
-    num_pages, Hkv, P, D2 = k_pages.shape
-    if D2 != D:
-        raise ValueError(f"k_pages has head_dim {D2}, q has {D}")
-    max_blocks = block_table.shape[1]
-    dev, dtype, need = _device_of(q), q.dtype, _fast_need
-    q_ptr = need(q, "q", dev, None, None)
-    sums = (B, Hkv, max_blocks * P)
-    in_ptr = out_ptr = need(weight_sums, "weight_sums", dev, _F32, sums)
     if sums_out is None:
         sums_out = weight_sums
-    else:
-        out_ptr = need(sums_out, "sums_out", dev, _F32, sums)
-    st = _pycall.attn_chunk_weights(
-        q_ptr, need(k_pages, "k_pages", dev, dtype, None),
-        need(block_table, "block_table", dev, _I32, (B, max_blocks)),
-        need(prefix_lens, "prefix_lens", dev, _I32, (B,)),
-        None if chunk_lens is None else need(chunk_lens, "chunk_lens", dev, _I32, (B,)),
-        need(lse, "lse", dev, _F32, (B, Hq, C)), in_ptr, out_ptr, B, C, int(window), max_blocks, num_pages, Hq,
-        Hkv, D, P, float(scale), float(decay), _dt(q), _ptr(err_flag), _stream(stream, dev))
-    _check(st, "attn_chunk_weights")
+    _check(_pycall.chunk_weights(q, k_pages, block_table, prefix_lens, chunk_lens, lse, weight_sums, sums_out, scale, decay,
+                                 window, err_flag, stream), "attn_chunk_weights")
     return sums_out
 
 
@@ -544,26 +444,16 @@ def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_t
                 kept=None, new_lens=None, new_sums=None, err_flag=None, stream=None):
     """Cuts every sequence to ``budget`` tokens per KV head, moved to the pages of
     ``new_block_table``, through ``attn_cache_evict``. Returns ``(kept, new_lens, new_sums)``."""
-    num_pages, Hkv, P, D = k_pages.shape
-    B, max_blocks = block_table.shape
-    new_blocks = new_block_table.shape[1]
-    dev, need, budget = _device_of(k_pages), _fast_need, int(budget)
-    k_ptr = need(k_pages, "k_pages", dev, None, None)
-    if kept is None:
-        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=_I32, device=k_pages.device)
-    if new_lens is None:
-        new_lens = torch.empty((B,), dtype=_I32, device=k_pages.device)
-    if new_sums is None:
-        new_sums = torch.empty((B, Hkv, new_blocks * P), dtype=_F32, device=k_pages.device)
-    st = _pycall.attn_cache_evict(
-        k_ptr, need(v_pages, "v_pages", dev, k_pages.dtype, k_pages.shape),
-        need(block_table, "block_table", dev, _I32, None), need(kv_lens, "kv_lens", dev, _I32, (B,)),
-        need(weight_sums, "weight_sums", dev, _F32, (B, Hkv, max_blocks * P)),
-        need(new_block_table, "new_block_table", dev, _I32, (B, new_blocks)),
-        need(kept, "kept", dev, _I32, (B, Hkv, max(budget, 0))), need(new_lens, "new_lens", dev, _I32, (B,)),
-        need(new_sums, "new_sums", dev, _F32, (B, Hkv, new_blocks * P)), B, max_blocks, new_blocks, num_pages, Hkv, D, P,
-        budget, int(n_sink), int(n_recent), _dt(k_pages), _ptr(err_flag), _stream(stream, dev))
-    _check(st, "attn_cache_evict")
+    if kept is None or new_lens is None or new_sums is None:
+        rows, dev = (block_table.shape[0], k_pages.shape[1]), k_pages.device
+        if kept is None:
+            kept = torch.empty((*rows, max(int(budget), 0)), dtype=torch.int32, device=dev)
+        if new_lens is None:
+            new_lens = torch.empty(rows[:1], dtype=torch.int32, device=dev)
+        if new_sums is None:
+            new_sums = torch.empty((*rows, new_block_table.shape[1] * k_pages.shape[2]), dtype=torch.float32, device=dev)
+    _check(_pycall.cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_table, kept, new_lens, new_sums,
+                               budget, n_sink, n_recent, err_flag, stream), "attn_cache_evict")
     return kept, new_lens, new_sums
 
 
@@ -575,20 +465,12 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 def linear(x, w, bias=None, activation="none", residual=None, out=None, err_flag=None, stream=None):
     """``act(x w^T + bias) + residual`` through ``attn_linear``: ``x`` ``[m, k]``, ``w`` ``[n, k]``,
     bf16; ``activation`` one of ``ACTIVATIONS``. ``out`` may be ``residual``."""
-    m, k = x.shape
-    n = w.shape[0]
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r}, one of {sorted(ACTIVATIONS)}")
-    dev, dtype, need = _device_of(x), x.dtype, _fast_need
-    x_ptr = need(x, "x", dev, None, None)
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=x.device)
-    st = _pycall.attn_linear(
-        x_ptr, need(w, "w", dev, dtype, (n, k)), None if bias is None else need(bias, "bias", dev, dtype, (n,)),
-        None if residual is None else need(residual, "residual", dev, dtype, (m, n)), need(out, "out", dev, dtype, (m, n)),
-        m, n, k, act, _dt(x), _ptr(err_flag), _stream(stream, dev))
-    _check(st, "attn_linear")
+        out = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
+    _check(_pycall.linear(x, w, bias, residual, out, act, err_flag, stream), "attn_linear")
     return out
 
 

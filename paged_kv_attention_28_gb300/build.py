@@ -101,7 +101,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
     tmp = PYCALL + ".tmp"
     # PyTorch's libraries are those that the importing process has loaded: no run path for them
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, module[1], "-L", PKG, "-l:libpkvattn.so",
-           "-Wl,-rpath,$ORIGIN", "-L", torch_lib(), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           "-Wl,-rpath,$ORIGIN", "-L", torch_lib(), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)

@@ -190,26 +190,28 @@ def test_empty_calls_do_nothing(b):
     assert err == 0 and torch.equal(out, c.q_out) and torch.equal(kp, c.k_pages) and torch.equal(vp, c.v_pages)
 
 
-def test_native_checks_of_real_tensors():
-    """The checks that read a tensor directly agree with what the tensor says of itself."""
+def test_native_checks_of_real_tensors(b):
+    """The call's quick look at its tensors, and what it says of those that are not in order."""
     from paged_kv_attention_28_gb300 import _pycall
-    x = torch.zeros(3, 5, 8, 16, dtype=torch.bfloat16, device="cuda")
-    bf, dims = torch.bfloat16, (3, 5, 8, 16)
-    for d, s in ((bf, dims), (None, None), (bf, None), (None, x.shape)):
-        assert _pycall.need(x, "x", 0, d, s) == x.data_ptr()
-    assert _pycall.need(x[1:], "x", 0, bf, (2, 5, 8, 16)) == x[1:].data_ptr()
-    assert _pycall.need(x[:0], "x", 0, bf, (0, 5, 8, 16)) == x[:0].data_ptr()
-    for t, dev, d, s in ((x, 1, bf, dims), (x, 0, torch.float16, dims), (x, 0, bf, (3, 5, 8, 8)), (x, 0, bf, (3, 5, 128)),
-                         (x, 0, bf, (3, 5, 8, 1 << 70)), (x[:, ::2], 0, bf, None), (x.transpose(0, 1), 0, bf, None)):
+    bf, dev = torch.bfloat16, "cuda"
+    x, w = torch.randn(4, 64, dtype=bf, device=dev), torch.randn(16, 64, dtype=bf, device=dev)
+    y, bias = torch.empty(4, 16, dtype=bf, device=dev), torch.zeros(16, dtype=bf, device=dev)
+    flag = torch.zeros(1, dtype=torch.int32, device=dev)
+    good = [x, w, bias, y, y, 0, flag, None]
+    assert _pycall.linear(*good) == 0 and _pycall.linear(x, w, None, None, y, 0, None, torch.cuda.current_stream()) == 0
+    for at, bad in ((0, x.float()), (0, x[:, ::2]), (0, x.T), (0, x.cpu()), (1, w.float()), (1, w[:, :32]), (1, w.cpu()),
+                    (1, w.T.contiguous().T), (2, bias[:8]), (2, bias.float()), (2, bias[None]), (3, y.T), (3, y[:2]), (4, y.cpu()),
+                    (4, y.half()), (4, y[:, :8]), (6, flag.float()), (6, flag.cpu())):
         with pytest.raises(ValueError):
-            _pycall.need(t, "x", dev, d, s)
-    fused = torch.zeros(3, 5, 24, 16, dtype=torch.bfloat16, device="cuda")
-    assert _pycall.rows(x, 0, bf, dims)[1] == 128
-    assert _pycall.rows(fused[:, :, 8:16], 0, bf, dims)[1] == 24 * 16
-    assert _pycall.rows(fused[:, :1, 8:16], 0, bf, (3, 1, 8, 16))[1] == 5 * 24 * 16
-    assert _pycall.rows(fused[:1, :1, 8:16], 0, bf, (1, 1, 8, 16))[1] == 8 * 16
-    for t, s in ((fused[:, :4, 8:16], (3, 4, 8, 16)), (fused[:, :, 8:16:2], (3, 5, 4, 16)), (fused[..., :8], (3, 5, 24, 8)),
-                 (x, (3, 5, 16, 8))):
-        assert _pycall.rows(t, 0, bf, s) is None
-    assert _pycall.rows(x, 1, bf, dims) is None and _pycall.rows(x, 0, torch.float16, dims) is None
-    assert _pycall.rows(fused[:, :, 8:16], 0, bf, dims)[0] == fused[:, :, 8:16].data_ptr()
+            _pycall.linear(*good[:at], bad, *good[at + 1:])
+    for at, bad in ((0, None), (4, None), (5, "relu"), (5, None), (6, 3), (7, 3)):
+        with pytest.raises((TypeError, ValueError, AttributeError)):
+            _pycall.linear(*good[:at], bad, *good[at + 1:])
+    assert _pycall.linear(*good[:5], (1 << 32) + 1, flag, None) == b.PKV_ERR_INVALID_ARG  # does not wrap
+    for t, d, s in ((x, bf, (4, 64)), (x, None, None), (x[:0], bf, (0, 64)), (x[1:], bf, x[1:].shape)):
+        assert _pycall.need(t, "x", 0, d, s) == t.data_ptr()
+    for t, d, s in ((x, torch.float16, None), (x, bf, (64, 4)), (x, bf, (4, 1 << 70)), (x[:, ::2], bf, None)):
+        with pytest.raises(ValueError):
+            _pycall.need(t, "x", 0, d, s)
+    with pytest.raises(ValueError, match="current device"):
+        _pycall.need(x, "x", 1, bf, None)
