@@ -205,6 +205,39 @@ def test_evict_orders_ties_and_odd_values(b, kind, lens, budget):
     check_evict(b, lens, 2, 64, "bf16", budget, 3, 11, kind=kind)
 
 
+@pytest.mark.parametrize("top", [0x3f81, 0xff7f, 0x8000])  # 1.0078 ..., the most negative numbers, -0 and below
+@pytest.mark.parametrize("few", [1, 2, 127, 128, 129, 300])
+@pytest.mark.parametrize("n", [900, 5000])
+def test_evict_among_keys_that_share_their_leading_digits(b, top, few, n):
+    """`few` sums share 16 bits, some of them all 32; the budget ends among them, at every place."""
+    g = torch.Generator().manual_seed(few)
+    order = torch.randperm(n, generator=g)
+    bits = torch.full((n,), 0x40000000, dtype=torch.int64) + torch.arange(n) * 4096  # above: 2 and more
+    bits[n // 2:] = 0xff7fffff if top != 0xff7f else 0xff800000  # below: the lowest number, -infinity
+    bits[n // 4:n // 4 + few] = (top << 16) + torch.randint(0, max(2, few // 2), (few,), generator=g) * 97
+    row = (bits - (bits >= 1 << 31) * (1 << 32)).to(torch.int32).view(torch.float32)[order]
+    sums = row.repeat(1, 1, 1)
+    pad = (n + 15) // 16 * 16 - n
+    sums = torch.cat((sums, torch.full((1, 1, pad), float("nan"))), -1).cuda()
+    blocks = (n + 15) // 16
+    kp = torch.zeros(blocks, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda").view(1, -1)
+    above = int((row > (torch.tensor([top << 16 if top < 0x8000 else (top << 16) - (1 << 32)], dtype=torch.int64)
+                        .to(torch.int32).view(torch.float32))).sum())
+    for budget in sorted({max(1, above - few), max(1, above - 1), above + 1, above + few // 2, above + few, n // 2 + few}):
+        if budget >= n:
+            continue
+        nb = (budget + 15) // 16
+        new = torch.arange(nb, dtype=torch.int32, device="cuda").view(1, -1)  # (what moves is not looked at)
+        spare = torch.zeros(nb, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+        pool = torch.cat((kp, spare))
+        kept, _, ns = b.cache_evict(pool, pool.clone(), table, torch.tensor([n], dtype=torch.int32, device="cuda"), sums,
+                                    new + blocks, budget)
+        wk, _, wn = oracle.evict(np.array([n]), sums.cpu().numpy(), budget, 0, 0)
+        assert kept[0, 0].tolist() == wk[0], budget
+        assert np.array_equal(ns[0, 0, :budget].cpu().numpy(), np.array(wn[0], dtype=np.float32))
+
+
 @pytest.mark.parametrize("sink,recent,budget", [(16, 32, 48), (0, 48, 48), (48, 0, 48), (16, 31, 48), (0, 0, 48)])
 def test_evict_when_sinks_and_recents_fill_the_budget(b, sink, recent, budget):
     check_evict(b, [700, 49, 5000], 2, 64, "bf16", budget, sink, recent, kind="odd")
