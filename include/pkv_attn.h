@@ -427,7 +427,8 @@ int attn_flat_gemm(const void* x, const void* w, void* y, int m, int n, int k, i
  *   chunk_lens   : int32 [batch], new tokens of each sequence (0 .. chunk_len), the rest of
  *                  its row being padding; NULL: chunk_len each
  *   q_out        : dtype [batch][chunk_len][n_qo_heads][head_dim], contiguous, aligned like
- *                  q; may be q itself when q_stride = n_qo_heads * head_dim. Padding rows are
+ *                  q; may be q itself when q_stride = n_qo_heads * head_dim, and must not overlap
+ *                  another input or a pool (their addresses are refused). Padding rows are
  *                  left as they were
  *   k_pages, v_pages, block_table : the paged layout above (16-byte aligned pools)
  * A sequence with prefix_lens[b] < 0, chunk_lens[b] outside its range, or prefix_lens[b] +
@@ -461,8 +462,8 @@ int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_
  * the newest token must have been set (to 0) before. sums_out may be sums_in (in place), and
  * must not overlap it otherwise. decay is finite (1: plain accumulation). out, lse, splits and
  * errors are as for attn_decode_paged (out is closer to the exact value than that call's where
- * the tensor cores take the weights: two bf16 parts of each, not one); a row that came out NaN makes its group's sums NaN, and
- * a bad length leaves the sequence's sums as they were. workspace: at least
+ * the tensor cores take the weights: two bf16 parts of each, not one); a row that came out
+ * NaN makes its group's sums NaN, and a bad length leaves the sequence's sums as they were. workspace: at least
  * attn_decode_weights_workspace_size bytes, 256-byte aligned: the split partials, the call's
  * logits (fp32 [batch][n_qo_heads][max_blocks_per_seq * page_size]) and log-sum-exps.
  */
@@ -523,8 +524,8 @@ int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_
  *   new_lens        : int32 [batch], out: min(n, budget)
  *   new_sums        : fp32 [batch][n_kv_heads][new_max_blocks * page_size], out: the kept
  *                     tokens' sums, 0 at and past the new length
- * Outputs must not overlap inputs (the same address is refused). A length < 0 or past the table sets PKV_DEVERR_BAD_LEN and
- * counts as 0. A bad entry of block_table sets PKV_DEVERR_BAD_PAGE and makes the rows NaN; a bad
+ * Outputs must not overlap inputs (the same address is refused). A length < 0 or past the
+ * table sets PKV_DEVERR_BAD_LEN and counts as 0. A bad entry of block_table sets PKV_DEVERR_BAD_PAGE and makes the rows NaN; a bad
  * entry of new_block_table sets it too and its rows are not copied.
  */
 int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
@@ -541,7 +542,8 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
  *   x : bf16 [m][k];  w : bf16 [n][k] (16-byte aligned both)
  *   bias : bf16 [n], or NULL;  residual : bf16 [m][n], or NULL (2-byte aligned both)
  *   activation : PKV_ACT_*
- *   y : bf16 [m][n]; may be residual itself, and must not overlap an input otherwise
+ *   y : bf16 [m][n]; may be residual itself, and must not overlap an input otherwise (the
+ *     address of x, w or bias is refused)
  * The product accumulates in fp32; bias, activation and residual are applied in fp32 and the
  * result is rounded once. k >= 1 a multiple of 8. m = 0 or n = 0 does nothing. err_flag
  * (nullable) gets PKV_DEVERR_TIMEOUT if a bounded wait gave up; the outputs affected are NaN.

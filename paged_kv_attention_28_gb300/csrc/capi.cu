@@ -514,6 +514,7 @@ int attn_linear(const void* x, const void* w, const void* bias, const void* resi
   if (m == 0 || n == 0) return PKV_OK;
   if (!x || !w || !y) return PKV_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w)) return PKV_ERR_INVALID_ARG;
+  if (y == x || y == w || y == bias) return PKV_ERR_INVALID_ARG;
   for (const void* p : {bias, residual, static_cast<const void*>(y)})
     if (reinterpret_cast<uintptr_t>(p) & 1) return PKV_ERR_INVALID_ARG;
   if (dtype != PKV_BF16 || k % 8) return PKV_ERR_UNSUPPORTED;
@@ -579,7 +580,8 @@ int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_
   const int64_t qw = (int64_t)n_qo_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
   if (q_stride < qw || k_stride < kw || v_stride < kw) return PKV_ERR_INVALID_ARG;
   if (q_stride % 4 || k_stride % 4 || v_stride % 4) return PKV_ERR_INVALID_ARG;
-  if (q_out == q && q_stride != qw) return PKV_ERR_INVALID_ARG;
+  if ((q_out == q && q_stride != qw) || q_out == k || q_out == v || q_out == k_pages || q_out == v_pages)
+    return PKV_ERR_INVALID_ARG;
   const uintptr_t quad = dtype == PKV_F32 ? 16 : 8;
   for (const void* p : {q, k, v, q_norm, k_norm, static_cast<const void*>(q_out)})
     if (reinterpret_cast<uintptr_t>(p) % quad) return PKV_ERR_INVALID_ARG;

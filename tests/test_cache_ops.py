@@ -21,6 +21,7 @@ def b():
 
 
 P = ctypes.c_void_p(1 << 20)
+P2 = ctypes.c_void_p(1 << 21)
 ODD = ctypes.c_void_p((1 << 20) + 4)
 P2, P3 = ctypes.c_void_p(1 << 21), ctypes.c_void_p(1 << 22)
 ODD1 = ctypes.c_void_p((1 << 20) + 1)
@@ -79,7 +80,7 @@ def test_linear_by_hand():
 
 def append_args(b, **kw):
     a = dict(q=P, k=P, v=P, qs=8 * 64, ks=2 * 64, vs=2 * 64, qn=None, kn=None, eps=1e-6, fr=P, rot=64, inter=0, pos=None,
-             axes=1, pa=None, bt=P, pl=P, cl=None, out=P, kp=P, vp=P, batch=1, chunk=1, mb=4, np=4, hq=8, hkv=2, d=64,
+             axes=1, pa=None, bt=P, pl=P, cl=None, out=P2, kp=P, vp=P, batch=1, chunk=1, mb=4, np=4, hq=8, hkv=2, d=64,
              page=16, dt=b.PKV_BF16)
     a.update(kw)
     return list(a.values()) + [None, None]
@@ -91,7 +92,7 @@ def append_args(b, **kw):
     (dict(hq=0), -1), (dict(dt=2), -1), (dict(rot=-8), -1), (dict(rot=72), -1), (dict(inter=2), -1), (dict(axes=0), -1),
     (dict(qs=8 * 64 - 4), -1), (dict(ks=64), -1), (dict(vs=130), -1), (dict(q=ODD), -1), (dict(k=ODD), -1),
     (dict(kp=ODD), -1), (dict(vp=ctypes.c_void_p((1 << 20) + 8)), -1), (dict(qn=P, eps=float("nan")), -1),
-    (dict(qn=P, eps=-1.0), -1), (dict(qn=ODD), -1), (dict(qs=1024, out=P), -1), (dict(mb=1 << 28), -1),
+    (dict(qn=P, eps=-1.0), -1), (dict(qn=ODD), -1), (dict(q=P2, qs=1024), -1), (dict(k=P2), -1), (dict(v=P2), -1), (dict(kp=P2), -1), (dict(vp=P2), -1), (dict(out=P), -1), (dict(mb=1 << 28), -1),
     (dict(d=96, qs=8 * 96, ks=192, vs=192), -2), (dict(page=32), -2), (dict(rot=12), -2), (dict(axes=5), -2),
     (dict(batch=1 << 17), -2), (dict(batch=0), 0), (dict(chunk=0, q=None), 0),
 ])
@@ -167,7 +168,7 @@ def test_chunk_weights_refuses(b, bad, want):
 
 
 def linear_args(b, **kw):
-    a = dict(x=P, w=P, bias=None, res=None, y=P, m=4, n=8, k=64, act=0, dt=b.PKV_BF16)
+    a = dict(x=P, w=P, bias=None, res=None, y=P2, m=4, n=8, k=64, act=0, dt=b.PKV_BF16)
     a.update(kw)
     return list(a.values()) + [None, None]
 
@@ -175,7 +176,7 @@ def linear_args(b, **kw):
 @pytest.mark.parametrize("bad,want", [
     (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(x=ODD), -1), (dict(w=ODD), -1), (dict(m=-1), -1),
     (dict(n=-1), -1), (dict(k=0), -1), (dict(act=5), -1), (dict(act=-1), -1), (dict(dt=3), -1),
-    (dict(y=ctypes.c_void_p((1 << 20) + 1)), -1), (dict(bias=ctypes.c_void_p((1 << 20) + 1)), -1),
+    (dict(y=ctypes.c_void_p((1 << 20) + 1)), -1), (dict(x=P2), -1), (dict(w=P2), -1), (dict(bias=P2), -1), (dict(bias=ctypes.c_void_p((1 << 20) + 1)), -1),
     (dict(k=12), -2), (dict(dt=0), -2), (dict(m=0, x=None), 0), (dict(n=0, w=None), 0),
 ])
 def test_linear_refuses(b, bad, want):
