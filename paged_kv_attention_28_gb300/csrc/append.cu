@@ -6,9 +6,11 @@
 //   z_a = y_a cos t - y_b sin t,  z_b = y_b cos t + y_a sin t  (each pair (a, b) of rotary_dim)
 //   t   = position[axis of the pair] * inv_freq[pair]
 // in fp32, rounded once to the row's type. Every element is read once and written once, so
-// the call is bound by those bytes: 4096 tokens (of 4 x 2048 padded) of 48 rows of 128 bf16, 101 MB, take 23 us,
-// 4.4 TB/s, where a copy takes 15; 62 % of the issue slots are taken and the rest is waiting for rows.
-// 64 tokens take 3.7 us, a launch.
+// the call is bound by those bytes: 8192 tokens of 48 rows of 128 bf16, 201 MB, take 42 us, 4.8 TB/s, half of
+// them (the rest padding) 23 us; 64 tokens 3.4 us, a launch. 62 % of the issue slots are taken. Not kept:
+// rows asked for two to four batches ahead through shared memory (1 to 15 % slower at twice the
+// warps, so it is not the loads' latency), two tokens at a time that share addresses and weights (7 %
+// slower: fewer warps).
 //
 // Angles: a position can be far (10^5 and more) and the angle matters modulo a full turn, so
 // an fp32 product loses what is needed (2^-24 of 10^5 rad is 0.006 rad). A pair's frequency is
