@@ -525,8 +525,9 @@ int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_
  *   new_sums        : fp32 [batch][n_kv_heads][new_max_blocks * page_size], out: the kept
  *                     tokens' sums, 0 at and past the new length
  * Outputs must not overlap inputs (the same address is refused). A length < 0 or past the
- * table sets PKV_DEVERR_BAD_LEN and counts as 0. A bad entry of block_table sets PKV_DEVERR_BAD_PAGE and makes the rows NaN; a bad
- * entry of new_block_table sets it too and its rows are not copied.
+ * table sets PKV_DEVERR_BAD_LEN and counts as 0. A bad entry of block_table sets
+ * PKV_DEVERR_BAD_PAGE and makes the rows NaN; a bad entry of new_block_table sets it too and
+ * its rows are not copied.
  */
 int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
                      const int32_t* kv_lens, const float* sums, const int32_t* new_block_table,

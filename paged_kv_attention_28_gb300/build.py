@@ -51,7 +51,8 @@ def _needs_rebuild(srcs) -> bool:
     if not os.path.exists(LIB) or not os.path.exists(PYCALL):
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
-    deps = srcs + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    deps = srcs + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+        glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(p) > t for p in deps)
 

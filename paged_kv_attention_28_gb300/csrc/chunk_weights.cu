@@ -64,13 +64,13 @@ constexpr int NKS = 4, NQS = 2;
 static_assert(NKS % 2 == 0, "a K stage belongs to one issuer");
 constexpr int CTHREADS = 640;
 // barriers
-constexpr int C_KF = 0, C_KE = C_KF + NKS, C_QF = C_KE + NKS, C_QE = C_QF + NQS, C_SF = C_QE + NQS, C_SE = C_SF + 4, C_DR = C_SE + 4, C_HF = C_DR + 1,
-              C_NBAR = C_HF + 8 * 3;
+constexpr int C_KF = 0, C_KE = C_KF + NKS, C_QF = C_KE + NKS, C_QE = C_QF + NQS, C_SF = C_QE + NQS, C_SE = C_SF + 4,
+              C_DR = C_SE + 4, C_HF = C_DR + 1, C_NBAR = C_HF + 8 * 3;
 constexpr int CITEMS = 256;            // items of a CTA
 constexpr int CWARPS = 16;             // exponential warps, four .. nineteen
-constexpr int SM_K = 0, SM_Q = SM_K + NKS * KSTG, SM_L = SM_Q + NQS * QSTG, SM_X = SM_L + CWARPS * CN * 4, SM_ITEM = SM_X + 4 * CK * 4,
-              SM_BAR = SM_ITEM + CITEMS * 64,
-              SM_MISC = SM_BAR + C_NBAR * 8, C_SMEM = SM_MISC + 16 + 1024;
+constexpr int SM_K = 0, SM_Q = SM_K + NKS * KSTG, SM_L = SM_Q + NQS * QSTG, SM_X = SM_L + CWARPS * CN * 4,
+              SM_ITEM = SM_X + 4 * CK * 4, SM_BAR = SM_ITEM + CITEMS * 64, SM_MISC = SM_BAR + C_NBAR * 8,
+              C_SMEM = SM_MISC + 16 + 1024;
 static_assert(C_SMEM <= 232448, "shared memory per CTA");
 constexpr float kL2e = 1.4426950408889634f;
 
@@ -543,13 +543,13 @@ int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream) {
     static FuncConfigured configured;
     if (!configured.ensure(reinterpret_cast<const void*>(chunk_weights_kernel<false>), C_SMEM)) return PKV_ERR_LAUNCH;
     const int64_t grid = n_tiles * rows < sms * waves ? n_tiles * rows : sms * waves;
-    return check_launch(
-        launch_overlapped(chunk_weights_kernel<false>, dim3((unsigned)grid), CTHREADS, C_SMEM, stream, 1, mq, mk, a, (int)(n_tiles * rows), 0));
+    return check_launch(launch_overlapped(chunk_weights_kernel<false>, dim3((unsigned)grid), CTHREADS, C_SMEM, stream, 1,
+                                          mq, mk, a, (int)(n_tiles * rows), 0));
   }
   static FuncConfigured configured;
   if (!configured.ensure(reinterpret_cast<const void*>(chunk_weights_kernel<true>), C_SMEM)) return PKV_ERR_LAUNCH;
-  return check_launch(launch_overlapped(chunk_weights_kernel<true>, dim3((unsigned)(n_tiles * rows << s_log2)), CTHREADS, C_SMEM,
-                                        stream, 1 << s_log2, mq, mk, a, (int)(n_tiles * rows), s_log2));
+  return check_launch(launch_overlapped(chunk_weights_kernel<true>, dim3((unsigned)(n_tiles * rows << s_log2)),
+                                        CTHREADS, C_SMEM, stream, 1 << s_log2, mq, mk, a, (int)(n_tiles * rows), s_log2));
 }
 
 }  // namespace pkv

@@ -10,11 +10,11 @@
 // and recents, so that what is kept is the `budget` largest keys. The last of them is searched
 // for by passes of 8 bits, each a histogram of the keys that share the digits found so far,
 // until a pass needs a whole bin or leaves few keys, which are then compared with one another
-// (rows of 20 tokens: 6.1 to 5.0 us a call; rows of 16-32k: 1.5 us of 103). Sums cluster (many are equal, most share an exponent) and
-// atomics on one address take turns, so a bin has 8 counters, by lane. Then each warp, which holds a
-// contiguous run of tokens, counts what it keeps, one scan over the warps places the runs, and
-// the kept indices and sums are written in order. Rows past kSmemTokens are read again in
-// each pass.
+// (rows of 20 tokens: 6.1 to 5.0 us a call; rows of 16-32k: 1.5 us of 103). Sums cluster (many are
+// equal, most share an exponent) and atomics on one address take turns, so a bin has 8 counters, by
+// lane. Then each warp, which holds a contiguous run of tokens, counts what it keeps, one scan over
+// the warps places the runs, and the kept indices and sums are written in order. Rows past
+// kSmemTokens are read again in each pass.
 //
 // What bounds the selection: the atomics and the emission of long rows (20 us for 16 x 8 rows of
 // 16-32k tokens), for short ones the instructions that every warp runs for a few tokens each, so
@@ -369,7 +369,8 @@ int launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const dim3 grid((unsigned)a.n_kv_heads, (unsigned)a.batch);
   int rc;
   if (cap <= kShortTokens) {
-    rc = check_launch(launch_overlapped(select_kernel<true, 256>, grid, 256, (size_t)((cap + 1023) / 1024) * 4096, stream, 1, a));
+    rc = check_launch(
+        launch_overlapped(select_kernel<true, 256>, grid, 256, (size_t)((cap + 1023) / 1024) * 4096, stream, 1, a));
   } else if (cap <= kSmemTokens) {
     static FuncConfigured configured;
     if (!configured.ensure(reinterpret_cast<const void*>(select_kernel<true, 1024>), kSmemTokens * 4))
