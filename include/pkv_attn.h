@@ -548,7 +548,8 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
  * The product accumulates in fp32; bias, activation and residual are applied in fp32 and the
  * result is rounded once. k >= 1 a multiple of 8. m = 0 or n = 0 does nothing. err_flag
  * (nullable) gets PKV_DEVERR_TIMEOUT if a bounded wait gave up; the outputs affected are NaN.
- * Up to 64 tokens run as attn_flat_gemm does, more on a tiled kernel.
+ * Few tokens (at most 64) run as attn_flat_gemm does where the weights' stream is most of the
+ * time, the rest on a tiled kernel.
  */
 int attn_linear(const void* x, const void* w, const void* bias, const void* residual, void* y,
                 int m, int n, int k, int activation, int dtype, int32_t* err_flag, void* stream);

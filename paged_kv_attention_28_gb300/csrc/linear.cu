@@ -1,7 +1,7 @@
 // Linear layer with its epilogue: y[m][n] = act(x[m][k] w[n][k]^T + bias[n]) + residual[m][n].
 //
-// Up to 64 tokens the weights stream through the tensor cores as in the flat GEMM (flat_gemm.cu
-// with its epilogue instantiation). Above, this file's kernel: persistent pairs of CTAs, a tile of
+// For few tokens the weights stream through the tensor cores as in the flat GEMM (flat_gemm.cu
+// with its epilogue instantiation; launch_linear has the rule). Else this file's kernel: persistent pairs of CTAs, a tile of
 // 256 tokens x BN features per pair. One tcgen05 product spans both SMs of the pair: each holds its
 // 128 tokens and half of the features, so that a CTA reads half the weights a single one would, and
 // the fp32 accumulators of its tokens. Operands come by TMA through a ring of six 64-column blocks;
@@ -15,7 +15,8 @@
 // rounds of tiles over the pairs take least (choose_width); what is lost is the last round: 1024 x 4096
 // x 4096 takes 24 us where its products are 18. A short product is bound by its epilogue, whose loads
 // are a chain: 2611 x 11008 x 256 takes 28 us, 50 with a residual (46 and 77 with four warps that ask for
-// everything when they need it), of which the products with their operands from the L2 are 17. Not
+// everything when they need it), of which the products with their operands from the L2 are 17. Rows
+// that no 16-byte store fits go through shared memory (1152 x 4097 x 1024 with residual: 75 to 31 us). Not
 // kept: sixteen warps (no faster, small products 3 % slower), y through shared memory and TMA (the same
 // time where rows are aligned to 32 bytes).
 #include <cuda.h>
@@ -64,8 +65,10 @@ __device__ __forceinline__ void tile_at(int i, int tiles_m, int tiles_n, int& tm
 
 // 32 features of one token, those from `end` on not stored. `bias` holds theirs (0 from `end` on); `res`
 // the residual's, where they are all stored and its rows are aligned.
-__device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[32], const float* bias, const uint4 (&res)[4], int row,
-                                           int col, int end) {
+// All lanes of a warp take part, those of tokens past the last too; `turn` is the warp's own corner of
+// shared memory, 32 x 17 floats.
+__device__ __forceinline__ void finish_rows(const LinArgs& a, float (&v)[32], const float* bias, const uint4 (&res)[4],
+                                            float* turn, int row, int col, int end) {
   constexpr int N = 32;
   const int64_t at = (int64_t)row * a.n + col;
   if (a.ep.bias) {
@@ -77,6 +80,7 @@ __device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[32], con
   }
   activate_all(v, a.ep.activation);
   if (a.vec && col + N <= end) {
+    if (row >= a.m) return;
     if (a.ep.residual) {
 #pragma unroll
       for (int i = 0; i < N; i += 8) {
@@ -105,11 +109,29 @@ __device__ __forceinline__ void finish_row(const LinArgs& a, float (&v)[32], con
         *reinterpret_cast<uint4*>(a.y + at + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
   } else {
+    // Rows that no wide store fits: through shared memory in two halves, so that a warp reads and
+    // writes runs of 16 features of two tokens at a time, not 32 tokens' single features.
+    constexpr int H = N / 2;
+    const int lane = threadIdx.x & 31, row0 = row - lane, c = lane % H;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (col + i < end) {
-        const float r = a.ep.residual ? __bfloat162float(a.ep.residual[at + i]) : 0.0f;
-        a.y[at + i] = __float2bfloat16_rn(a.ep.residual ? v[i] + r : v[i]);
+    for (int half = 0; half < 2; ++half) {
+      const int f = col + half * H + c;
+      const int64_t to = (int64_t)(row0 + lane / H) * a.n + f;  // of the lane's first token
+      float add[H] = {};
+      if (a.ep.residual) {  // all asked for before any is used: y may be the residual
+#pragma unroll
+        for (int i = 0; i < H; ++i)
+          if (row0 + lane / H + 2 * i < a.m && f < end) add[i] = __bfloat162float(a.ep.residual[to + (int64_t)(2 * i) * a.n]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < H; ++i) turn[lane * (H + 1) + i] = v[half * H + i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float x = turn[(lane / H + 2 * i) * (H + 1) + c];
+        if (row0 + lane / H + 2 * i < a.m && f < end)
+          a.y[to + (int64_t)(2 * i) * a.n] = __float2bfloat16_rn(a.ep.residual ? x + add[i] : x);
       }
     }
   }
@@ -124,7 +146,8 @@ struct LinCfg {
   static constexpr int PST = 6 / SUB, STG = SUB * BLK;  // stages; bytes of one operand's stage
   static constexpr int SM_B = PST * STG, SM_BAR = 2 * PST * STG, NBAR = 2 * PST + 5, SM_MISC = SM_BAR + NBAR * 8,
                        SM_BIAS = (SM_MISC + 16 + 15) / 16 * 16,  // [8 warps][4 runs][32]
-                       SMEM = SM_BIAS + 8 * 4 * 32 * 4 + 1024;
+                       SM_TURN = SM_BIAS + 8 * 4 * 32 * 4,       // [8 warps][32][17]
+                       SMEM = SM_TURN + 8 * 32 * 17 * 4 + 1024;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -310,6 +333,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     // before and to registers two runs ahead.
     const int wq = warp & 3, group = (warp - 4) >> 2;
     float* bias_s = reinterpret_cast<float*>(smem + C::SM_BIAS) + (warp - 4) * 128;
+    float* turn_s = reinterpret_cast<float*>(smem + C::SM_TURN) + (warp - 4) * (32 * 17);
     float bias_next[4] = {};
     auto ask_bias = [&](int col0, int end) {
 #pragma unroll
@@ -364,7 +388,7 @@ linear_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
         float v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = ok ? __uint_as_float(r[k]) : NAN;
-        if (row < a.m && col0 + cc < end) finish_row(a, v, bias_s + cc / 64 * 32, res, row, col0 + cc, end);
+        if (col0 + cc < end) finish_rows(a, v, bias_s + cc / 64 * 32, res, turn_s, row, col0 + cc, end);
 #pragma unroll
         for (int k = 0; k < 4; ++k) res[k] = next_res[k];
         ask(next_res, cc + 128);
@@ -430,7 +454,13 @@ constexpr int kWide = 224;  // tiles from this width take one block per stage
 }  // namespace
 
 int launch_linear(const LinearArgs& p, cudaStream_t stream) {
-  if (p.m <= kFlatGemmMaxM) return launch_flat_linear(p, stream);
+  // Few tokens stream the weights (flat_gemm.cu) where that is most of the time. Its reduction over a
+  // cluster and its epilogue, which grows with the tokens, cost more than a tile here for short products,
+  // and past 32 tokens for all but long ones. There and here, in us: 8 x 1024 x 72 5.8 and 5.2, 40 x 1024 x 72
+  // 11.6 and 4.9, 64 x 4096 x 512 10.5 and 6.8, 64 x 11008 x 1024 14.6 and 9.0; but 8 x 1024 x 1024 5.5 and 7.3,
+  // 32 x 4096 x 4096 11 and 13, 64 x 4096 x 4096 with cold weights 21 and 25, 64 x 1024 x 8192 12.6 and 19.5.
+  const bool tiled = p.k <= 128 || (p.m > 32 && (p.k <= 1024 || p.k <= p.n / 2));
+  if (p.m <= kFlatGemmMaxM && !tiled) return launch_flat_linear(p, stream);
   if (p.m > 0x7fffff00 || p.n > 0x7fffff00) return PKV_ERR_UNSUPPORTED;  // (tile ends fit 32 bits)
   int sms = device_sm_count();
   if (sms <= 1) sms = 148;

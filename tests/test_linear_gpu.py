@@ -125,3 +125,20 @@ def test_linear_in_a_graph(b, m):
     g.replay()
     torch.cuda.synchronize()
     check(y, x2, w, bi, "silu", re)
+
+
+@pytest.mark.parametrize("m", [1, 32, 33, 64, 65])
+@pytest.mark.parametrize("n,k", [(1024, 128), (1024, 136), (1000, 1024), (1000, 1032), (2064, 1032), (2062, 1032), (33, 72), (4097, 200)])
+def test_linear_on_both_sides_of_the_choice_of_kernel(b, m, n, k):
+    """Sizes beside the bounds at which another kernel takes over, with rows of every alignment and a residual in place."""
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    x, w = (torch.randn(*s, device="cuda", generator=g).bfloat16() for s in ((m, k), (n, k)))
+    bias, y = (torch.randn(*s, device="cuda", generator=g).bfloat16() for s in ((n,), (m, n)))
+    res = y.clone()
+    b.linear(x, w, bias, "relu", y, out=y)
+    z = x.double() @ w.double().T + bias.double()
+    want = z.clamp(min=0) + res.double()
+    # k products added in fp32 (each sum at most S, k roundings), bias and residual; one rounding to bf16
+    size = x.double().abs() @ w.double().abs().T + bias.double().abs() + res.double().abs()
+    bar = (k + 4) * 2.0 ** -24 * size + 2.0 ** -8 * want.abs()
+    assert bool(((y.double() - want).abs() <= bar).all())
