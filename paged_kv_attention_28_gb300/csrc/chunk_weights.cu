@@ -27,9 +27,9 @@
 // short ones: key tiles slowest (early keys are seen by the most queries), and every other round
 // of the CTAs backwards (135 to 108 us against a plain stride). All its threads work its list of
 // items out at the start, for every warp to read (16.3 to 13.7 us for the window: each warp working
-// them out by itself took longer than its step). With fewer items than half the SMs
-// an item's steps are shared by a cluster of 2 to 8 CTAs, whose partial sums are added in rank
-// order through distributed shared memory.
+// them out by itself took longer than its step). Few or uneven items are shared, each by a cluster
+// of 2 to 8 CTAs (choose_split), whose partial sums are added in rank order through distributed
+// shared memory.
 // Warps: 0 and 2 TMA producers (a ring of four K tiles, page by page, and one of two Q tiles), 1
 // and 3 MMA issuers of the two key tiles, 4..11 and 12..19 their exponentials and sums. S^T is
 // double-buffered per tile: all 512 TMEM columns.
@@ -37,6 +37,7 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "internal.h"
@@ -507,6 +508,45 @@ bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, c
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// log2 of the CTAs that share an item, from a chunk that fills the table. Estimated in 10 ns: a step takes
+// 100, a CTA's start 700, the next item of a persistent CTA 100 besides its steps; clusters of 2 and 4 can use
+// about 95 % of the SMs, of 8 84 %. Measured, whole and shared by 2, 4, 8, in us: 40 items of up to 73 steps 76,
+// 42, 26, 37; 128 of up to 128 steps 121, 66, 81, 121; 224 of up to 49 steps 94, 83, 105, 171; 224 of up to 64
+// steps 83, 87, 112, 171; 28 of up to 5 steps 12.4, 10.8, 10.7.
+int choose_split(const ChunkWeightsArgs& a, int64_t items, int64_t rows, int64_t n_tiles, int n_queries, int qpt, int sms) {
+  const int64_t prefix = std::max<int64_t>(0, (int64_t)a.max_blocks * a.page_size - a.chunk_len);
+  auto steps_of = [&](int64_t tile) {  // of the items of a key tile
+    const int64_t first = std::max<int64_t>(a.chunk_len - n_queries, tile * CK - prefix);
+    return first < a.chunk_len ? (a.chunk_len - first + qpt - 1) / qpt : 0;
+  };
+  const int64_t steps = steps_of(0);
+  if (steps < 2) return 0;
+  const int64_t seen = std::min<int64_t>(n_tiles, (n_queries + CK - 1) / CK);  // tiles that part of the queries see
+  const int64_t total = 100 * rows * (steps * (n_tiles - seen) + steps * seen / 2);
+  // whole items: the CTA with the most, exactly where there are few, else the mean
+  int64_t best = 0;
+  if (items <= 4 * (int64_t)sms) {
+    for (int i = 0; i < sms && i < items; ++i) {
+      int64_t sum = 0, at = i;
+      for (int odd = 0; at < items; odd ^= 1) {
+        sum += 100 * steps_of(at / rows) + 100;
+        at += odd ? 2 * i + 1 : 2 * (int64_t)sms - 1 - 2 * i;
+      }
+      best = std::max(best, sum);
+    }
+    best += 600;
+  } else {
+    best = 700 + (total + 100 * items) / sms;
+  }
+  int s_log2 = 0;
+  for (int s = 1; s <= 3 && (1 << s) <= steps && items << s <= 0x7fffffffL; ++s) {
+    const int64_t part = 100 * ((steps + (1 << s) - 1) >> s) + 700;
+    const int64_t cost = std::max(part, (total + 700 * (items << s)) / (sms * (s == 3 ? 84 : 95) / 100) + part / 4);
+    if (cost < best) best = cost, s_log2 = s;
+  }
+  return s_log2;
+}
+
 }  // namespace
 
 int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream) {
@@ -531,12 +571,8 @@ int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream) {
   if (rows > 0x3fffffffL || n_tiles * rows > 0x7fffffffL) return PKV_ERR_UNSUPPORTED;
   int sms = device_sm_count();
   if (sms <= 0) sms = 148;
-  // Few items: share the steps of each among the largest cluster that fits the SMs and leaves
-  // every CTA a step.
   const int n_queries = a.window > 0 && a.window < a.chunk_len ? a.window : a.chunk_len;
-  const int64_t steps = ((int64_t)n_queries * G + CN - 1) / CN;
-  int s_log2 = 0;
-  while (s_log2 < 3 && (2 << s_log2) <= steps && (n_tiles * rows << (s_log2 + 1)) <= sms) ++s_log2;
+  const int s_log2 = choose_split(a, n_tiles * rows, rows, n_tiles, n_queries, CN / G, sms);
   if (s_log2 == 0) {
     // a CTA per SM, more where the list of one cannot hold its share
     const int64_t waves = (n_tiles * rows + (int64_t)sms * (CITEMS - 2) - 1) / ((int64_t)sms * (CITEMS - 2));

@@ -215,3 +215,11 @@ def test_more_items_than_the_list_of_one_cta_per_sm(b):
     live = (torch.arange(16, device="cuda") <= pl[:, None])[:, None].expand_as(w)
     off = (got.double() - (w + sums.double())).abs()
     assert bool((off <= bar)[live].all()) and bool((got[~live] == 7.0).all())
+
+
+@pytest.mark.parametrize("prefix,chunk,hq,hkv,kw", [
+    ([40, 25], 500, 32, 4, {}), ([40, 25], 500, 32, 4, dict(chunk_lens=[500, 3])), ([0], 700, 32, 8, dict(in_place=False)),
+    ([900, 1, 300], 130, 64, 16, dict(window=129)), ([0, 0, 0, 0], 200, 16, 16, dict(chunk_lens=[200, 1, 0, 199])),
+])
+def test_items_shared_by_more_clusters_than_fit_at_once(b, prefix, chunk, hq, hkv, kw):
+    check(b, prefix, chunk, hq, hkv, **kw)
