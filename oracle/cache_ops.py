@@ -69,7 +69,7 @@ def key_weights(q, k_pages, block_table, lens, lse, scale, first=None, last=None
         lo, hi = (0 if first is None else int(first[b])), (C if last is None else int(last[b]))
         n = int(lens[b]) + hi
         for g in range(Hkv):
-            keys = np.array([k_pages[int(block_table[b][t // page]), g, t % page] for t in range(n)]).reshape(n, -1)
+            keys = np.array([k_pages[int(block_table[b][t // page]), g, t % page] for t in range(n)]).reshape(n, k_pages.shape[3])
             total = np.zeros(n)
             for i in range(lo, hi):
                 see = int(lens[b]) + i + 1
