@@ -542,7 +542,7 @@ int choose_split(const ChunkWeightsArgs& a, int64_t items, int64_t rows, int64_t
   for (int s = 1; s <= 3 && (1 << s) <= steps && items << s <= 0x7fffffffL; ++s) {
     const int64_t part = 100 * ((steps + (1 << s) - 1) >> s) + 700;
     const int64_t cost = std::max(part, (total + 700 * (items << s)) / (sms * (s == 3 ? 84 : 95) / 100) + part / 4);
-    if (cost < best) best = cost, s_log2 = s;
+    if (cost + cost / 20 < best) best = cost, s_log2 = s;  // (the estimate is off by a few per cent)
   }
   return s_log2;
 }
