@@ -3,7 +3,8 @@
 This layer only marshals arguments, through ctypes or, for the operators whose smallest calls
 take less time than that, through the CPython module ``_pycall`` (csrc/pycall.cpp). It turns torch CUDA tensors into device
 pointers, checks shapes and dtypes on the host, and passes the current CUDA
-stream. Every step of the computation runs in the library's kernels. If the
+stream, or ``stream`` (a torch stream, or an object with its ``cuda_stream`` handle), which also owns the
+buffers that the call makes for itself. Every step of the computation runs in the library's kernels. If the
 library is missing, importing this module raises; nothing falls back to
 another implementation.
 """
@@ -156,6 +157,22 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _empty(shape, dtype, device, stream, output=True):
+    """A buffer that a call makes for itself, in the memory of the stream that it runs on: memory of the
+    current stream could still be waiting for that stream's earlier work, and go to its next work while
+    the call uses it."""
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output and stream.cuda_stream != current.cuda_stream:
+        t.record_stream(current)  # it may be dropped while the caller's stream still reads it
+    return t
+
+
 # --------------------------------------------------------------------------- decode
 
 def decode_num_splits(batch, max_blocks, n_qo_heads, n_kv_heads, head_dim, page_size, num_splits=0,
@@ -175,11 +192,12 @@ def decode_workspace_size(batch, max_blocks, n_qo_heads, n_kv_heads, head_dim, p
     return n
 
 
-def alloc_workspace(nbytes: int, device) -> torch.Tensor | None:
-    """A 256-byte aligned device buffer (torch's allocator aligns to at least 512 bytes)."""
+def alloc_workspace(nbytes: int, device, stream=None) -> torch.Tensor | None:
+    """A 256-byte aligned device buffer (torch's allocator aligns to at least 512 bytes), for calls on
+    ``stream`` (None: the current one)."""
     if nbytes == 0:
         return None
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _empty(nbytes, torch.uint8, device, stream, output=False)
 
 
 def decode_paged(q, k_pages, v_pages, block_table, kv_lens, scale, num_splits=0, out=None,
@@ -197,12 +215,12 @@ def decode_paged(q, k_pages, v_pages, block_table, kv_lens, scale, num_splits=0,
     _need(block_table, "block_table", torch.int32, (B, max_blocks))
     _need(kv_lens, "kv_lens", torch.int32, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((B, Hq), torch.float32, q.device, stream)
     ws_bytes = decode_workspace_size(B, max_blocks, Hq, Hkv, D, P, num_splits, _dt(q))
     if workspace is None:
-        workspace = alloc_workspace(ws_bytes, q.device)
+        workspace = alloc_workspace(ws_bytes, q.device, stream)
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = [_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(kv_lens), _ptr(out),
             _ptr(lse), B, max_blocks, num_pages, Hq, Hkv, D, P, float(scale), int(num_splits), _dt(q)]
@@ -234,12 +252,12 @@ def decode_paged_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, kv_lens
     _need(block_table, "block_table", torch.int32, (B, max_blocks))
     _need(kv_lens, "kv_lens", torch.int32, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((B, Hq), torch.float32, q.device, stream)
     ws_bytes = decode_workspace_size(B, max_blocks, Hq, Hkv, D, P, num_splits, PKV_FP8_E4M3)
     if workspace is None:
-        workspace = alloc_workspace(ws_bytes, q.device)
+        workspace = alloc_workspace(ws_bytes, q.device, stream)
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib.attn_decode_paged_fp8(_ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
                                    _ptr(v_scale), _ptr(block_table), _ptr(kv_lens), _ptr(out),
@@ -260,9 +278,9 @@ def merge_states(out_a, lse_a, out_b, lse_b, out=None, lse=None, out_dtype=torch
     for t, n in ((lse_a, "lse_a"), (lse_b, "lse_b")):
         _need(t, n, torch.float32, out_a.shape[:-1])
     if out is None:
-        out = torch.empty(out_a.shape, dtype=out_dtype, device=out_a.device)
+        out = _empty(out_a.shape, out_dtype, out_a.device, stream)
     if lse is None:
-        lse = torch.empty(lse_a.shape, dtype=torch.float32, device=out_a.device)
+        lse = _empty(lse_a.shape, torch.float32, out_a.device, stream)
     st = lib.attn_merge_states(_ptr(out_a), _ptr(lse_a), _ptr(out_b), _ptr(lse_b), _ptr(out),
                                _ptr(lse), rows, D, _dt(out), _stream(stream))
     _check(st, "attn_merge_states")
@@ -279,9 +297,9 @@ def prefill_causal(q, k, v, scale, out=None, lse=None, err_flag=None, stream=Non
     _need(k, "k", q.dtype, (B, T, Hkv, D))
     _need(v, "v", q.dtype, (B, T, Hkv, D))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        lse = _empty((B, Hq, T), torch.float32, q.device, stream)
     st = lib.attn_prefill_causal(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, T, Hq, Hkv, D,
                                  float(scale), _dt(q), _ptr(err_flag), _stream(stream))
     _check(st, "attn_prefill_causal")
@@ -304,9 +322,9 @@ def prefill_paged_chunk(q, k_pages, v_pages, block_table, prefix_lens, scale, ou
     _need(block_table, "block_table", torch.int32, (B, max_blocks))
     _need(prefix_lens, "prefix_lens", torch.int32, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, C), dtype=torch.float32, device=q.device)
+        lse = _empty((B, Hq, C), torch.float32, q.device, stream)
     st = lib.attn_prefill_paged_chunk(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
                                       _ptr(prefix_lens), _ptr(out), _ptr(lse), B, C, max_blocks,
                                       num_pages, Hq, Hkv, D, P, float(scale), _dt(q), _ptr(err_flag),
@@ -340,12 +358,12 @@ def decode_cascade(q, k_pages, v_pages, prefix_table, prefix_len, suffix_table, 
     if prefix_len > 0:
         _need(prefix_table, "prefix_table", torch.int32)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((R, Hq), torch.float32, q.device, stream)
     nb = cascade_workspace_size(R, prefix_len, ms, Hq, Hkv, D, P)
     if workspace is None:
-        workspace = alloc_workspace(nb, q.device)
+        workspace = alloc_workspace(nb, q.device, stream)
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib.attn_decode_cascade(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(prefix_table),
                                  int(prefix_len), _ptr(suffix_table), _ptr(suffix_lens), _ptr(out),
@@ -372,7 +390,7 @@ def flat_gemm(x, w, out=None, err_flag=None, stream=None):
     _need(x, "x")
     _need(w, "w", x.dtype, (n, k))
     if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+        out = _empty((m, n), x.dtype, x.device, stream)
     _need(out, "out", x.dtype, (m, n))
     st = lib.attn_flat_gemm(_ptr(x), _ptr(w), _ptr(out), m, n, k, _dt(x), _ptr(err_flag), _stream(stream))
     _check(st, "attn_flat_gemm")
@@ -390,7 +408,7 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chu
     projection; ``positions`` ``[n_axes, B, C]`` (or ``[B, C]`` for one axis). Returns the
     rotated queries ``[B, C, Hq, D]``."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _check(_pycall.qk_norm_rope_append(q, k, v, k_pages, v_pages, block_table, prefix_lens, chunk_lens, positions, inv_freq,
                                        pair_axis, q_norm, k_norm, eps, interleaved, out, err_flag, stream),
            "attn_qk_norm_rope_append")
@@ -414,13 +432,13 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums,
     ``[B, Hkv, max_blocks * page_size]`` (in place, or into ``sums_out``), through
     ``attn_decode_paged_weights``. Returns ``(out, lse, sums)``."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = _empty(q.shape[:2], torch.float32, q.device, stream)
     if workspace is None:
         B, Hq, D = q.shape
         workspace = alloc_workspace(decode_weights_workspace_size(B, block_table.shape[1], Hq, k_pages.shape[1], D,
-                                                                  k_pages.shape[2], num_splits, _dt(q)), q.device)
+                                                                  k_pages.shape[2], num_splits, _dt(q)), q.device, stream)
     if sums_out is None:
         sums_out = weight_sums
     _check(_pycall.decode_paged_weights(q, k_pages, v_pages, block_table, kv_lens, weight_sums, sums_out, scale, decay,
@@ -447,11 +465,11 @@ def cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_t
     if kept is None or new_lens is None or new_sums is None:
         rows, dev = (block_table.shape[0], k_pages.shape[1]), k_pages.device
         if kept is None:
-            kept = torch.empty((*rows, max(int(budget), 0)), dtype=torch.int32, device=dev)
+            kept = _empty((*rows, max(int(budget), 0)), torch.int32, dev, stream)
         if new_lens is None:
-            new_lens = torch.empty(rows[:1], dtype=torch.int32, device=dev)
+            new_lens = _empty(rows[:1], torch.int32, dev, stream)
         if new_sums is None:
-            new_sums = torch.empty((*rows, new_block_table.shape[1] * k_pages.shape[2]), dtype=torch.float32, device=dev)
+            new_sums = _empty((*rows, new_block_table.shape[1] * k_pages.shape[2]), torch.float32, dev, stream)
     _check(_pycall.cache_evict(k_pages, v_pages, block_table, kv_lens, weight_sums, new_block_table, kept, new_lens, new_sums,
                                budget, n_sink, n_recent, err_flag, stream), "attn_cache_evict")
     return kept, new_lens, new_sums
@@ -469,7 +487,7 @@ def linear(x, w, bias=None, activation="none", residual=None, out=None, err_flag
     if act is None:
         raise ValueError(f"unknown activation {activation!r}, one of {sorted(ACTIVATIONS)}")
     if out is None:
-        out = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
+        out = _empty((x.shape[0], w.shape[0]), x.dtype, x.device, stream)
     _check(_pycall.linear(x, w, bias, residual, out, act, err_flag, stream), "attn_linear")
     return out
 
