@@ -365,8 +365,9 @@ int launch_fg(const FlatGemmArgs& p, const Epilogue& ep, const FlatGemmPlan& pla
 
 template <bool EPI>
 int launch_fg_any(const FlatGemmArgs& a, const Epilogue& ep, cudaStream_t stream) {
+  static_assert(kFlatGemmMaxN / FG_BM == 65535, "tiles of a grid");
+  if (a.n > kFlatGemmMaxN) return PKV_ERR_UNSUPPORTED;
   const FlatGemmPlan plan = plan_flat_gemm(a.m, a.n, a.k);
-  if (plan.tiles > 65535) return PKV_ERR_UNSUPPORTED;
   switch (flat_gemm_padded_m(a.m)) {
     case 16: return launch_fg<16, EPI>(a, ep, plan, stream);
     case 32: return launch_fg<32, EPI>(a, ep, plan, stream);

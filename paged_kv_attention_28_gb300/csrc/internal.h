@@ -192,6 +192,7 @@ struct FlatGemmPlan {
   int n_kc;        // 64-column slices of K in all
 };
 constexpr int kFlatGemmMaxM = 64;
+constexpr int kFlatGemmMaxN = 65535 * 128;  // its tiles of 128 features are the y of a grid
 int flat_gemm_padded_m(int m);
 FlatGemmPlan plan_flat_gemm(int m, int n, int k);
 int launch_flat_gemm(const FlatGemmArgs& a, cudaStream_t stream);
@@ -258,7 +259,7 @@ struct LinearArgs {
   int32_t* err_flag;
 };
 int launch_linear(const LinearArgs& a, cudaStream_t stream);
-// The same for m <= kFlatGemmMaxM, on the flat GEMM's kernel (flat_gemm.cu).
+// The same for m <= kFlatGemmMaxM and n <= kFlatGemmMaxN, on the flat GEMM's kernel (flat_gemm.cu).
 int launch_flat_linear(const LinearArgs& a, cudaStream_t stream);
 
 }  // namespace pkv

@@ -459,7 +459,8 @@ int launch_linear(const LinearArgs& p, cudaStream_t stream) {
   // and past 32 tokens for all but long ones. There and here, in us: 8 x 1024 x 72 5.8 and 5.2, 40 x 1024 x 72
   // 11.6 and 4.9, 64 x 4096 x 512 10.5 and 6.8, 64 x 11008 x 1024 14.6 and 9.0; but 8 x 1024 x 1024 5.5 and 7.3,
   // 32 x 4096 x 4096 11 and 13, 64 x 4096 x 4096 with cold weights 21 and 25, 64 x 1024 x 8192 12.6 and 19.5.
-  const bool tiled = p.k <= 128 || (p.m > 32 && (p.k <= 1024 || p.k <= p.n / 2));
+  // More features than the flat kernel's grid holds run here whatever their time.
+  const bool tiled = p.k <= 128 || (p.m > 32 && (p.k <= 1024 || p.k <= p.n / 2)) || p.n > kFlatGemmMaxN;
   if (p.m <= kFlatGemmMaxM && !tiled) return launch_flat_linear(p, stream);
   if (p.m > 0x7fffff00 || p.n > 0x7fffff00) return PKV_ERR_UNSUPPORTED;  // (tile ends fit 32 bits)
   int sms = device_sm_count();
