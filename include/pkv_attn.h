@@ -487,7 +487,9 @@ int attn_decode_paged_weights(const void* q, const void* k_pages, const void* v_
  * over the queries i >= t - prefix_lens[b] (the causal mask) among the last `window` of the
  * sequence's new tokens (window 0: all of them), for t < prefix_lens[b] + n; other slots are
  * neither read nor written. n = chunk_lens[b] where given (0 .. chunk_len; the rest of the
- * chunk is padding whose q and lse do not matter), else chunk_len.
+ * chunk is padding whose q and lse do not matter), else chunk_len. Without queries (n = 0, also by
+ * chunk_len = 0, where q and lse may be NULL) the sums of the prefix_lens[b] keys decay. (A call
+ * with chunk_len 0, decay 1 and sums in place has nothing to do and does not look at the lengths.)
  *
  *   q    : bf16 [batch][chunk_len][n_qo_heads][head_dim]
  *   lse  : fp32 [batch][n_qo_heads][chunk_len]

@@ -493,8 +493,11 @@ int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_
   if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
   if ((long)max_blocks_per_seq * page_size > 0x7fffffffL) return PKV_ERR_INVALID_ARG;
   if (chunk_len > max_blocks_per_seq * page_size) return PKV_ERR_INVALID_ARG;
-  if (batch == 0 || chunk_len == 0) return PKV_OK;
-  if (!q || !k_pages || !block_table || !prefix_lens || !lse || !sums_in || !sums_out) return PKV_ERR_INVALID_ARG;
+  if (batch == 0) return PKV_OK;
+  // (without queries nothing is left but the decay, and of that nothing in place at 1)
+  if (chunk_len == 0 && decay == 1.0f && sums_in == sums_out) return PKV_OK;
+  if (!k_pages || !block_table || !prefix_lens || !sums_in || !sums_out) return PKV_ERR_INVALID_ARG;
+  if (chunk_len > 0 && (!q || !lse)) return PKV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pages)) return PKV_ERR_INVALID_ARG;
   const int G = n_qo_heads / n_kv_heads;
   if (dtype != PKV_BF16 || head_dim != 128 || page_size != 16 || 128 % G) return PKV_ERR_UNSUPPORTED;

@@ -554,10 +554,12 @@ int launch_chunk_weights(const ChunkWeightsArgs& a, cudaStream_t stream) {
   CUtensorMap mq, mk;
   {
     // q [B][C][Hq][128] as (128, Hq, C, B): a box is 64 dims of the group's heads of qpt queries
-    cuuint64_t dims[4] = {CD, (cuuint64_t)a.n_qo_heads, (cuuint64_t)a.chunk_len, (cuuint64_t)a.batch};
-    cuuint64_t strides[3] = {CD * 2, (cuuint64_t)a.n_qo_heads * CD * 2, (cuuint64_t)a.chunk_len * a.n_qo_heads * CD * 2};
+    // (a chunk without queries loads none: any aligned address and length make a map)
+    const cuuint64_t chunk = (cuuint64_t)std::max(a.chunk_len, 1);
+    cuuint64_t dims[4] = {CD, (cuuint64_t)a.n_qo_heads, chunk, (cuuint64_t)a.batch};
+    cuuint64_t strides[3] = {CD * 2, (cuuint64_t)a.n_qo_heads * CD * 2, chunk * a.n_qo_heads * CD * 2};
     cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)(CN / G), 1};
-    if (!encode(&mq, a.q, 4, dims, strides, box)) return check_launch(cudaErrorInvalidValue);
+    if (!encode(&mq, a.chunk_len > 0 ? a.q : a.k_pages, 4, dims, strides, box)) return check_launch(cudaErrorInvalidValue);
   }
   {
     // pools as (64 dims, 8 rows, 2 halves, 8-row groups): a box is one (page, KV head) block

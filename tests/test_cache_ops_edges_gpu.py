@@ -41,3 +41,41 @@ def test_linear_with_more_features_than_the_few_token_kernel_has_tiles(b, m, act
     # k products added in fp32 and the bias, one rounding each at most S; one rounding to bf16
     bar = (k + 2) * 2.0 ** -24 * size + 2.0 ** -8 * want.abs()
     assert bool(((got.double() - want).abs() <= bar).all())
+
+
+# ------------------------------------------------------------------------------------ weights over a chunk
+
+@pytest.mark.parametrize("in_place,decay", [(True, 0.5), (False, 0.5), (False, 1.0), (True, 1.0)])
+@pytest.mark.parametrize("window", [0, 32])
+def test_an_empty_chunk_decays_the_sums(b, in_place, decay, window):
+    """chunk_len 0, and the same said by chunk_lens."""
+    lens, cap = [0, 1, 40, 640, 300], 640
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kp = torch.randn(200, 2, 16, 128, generator=g, device="cuda").bfloat16()
+    table = torch.arange(200, dtype=torch.int32, device="cuda").view(5, 40)
+    sums = torch.rand(5, 2, cap, generator=g, device="cuda")
+    want = sums * decay  # one rounding, as the call's
+    for chunk in (0, 3):
+        s = sums.clone()
+        o = s if in_place else torch.full_like(s, 7.0)
+        before = o.clone()
+        err = i32(0)
+        b.chunk_weights(torch.full((5, chunk, 8, 128), float("nan"), device="cuda").bfloat16(), kp, table, i32(*lens),
+                        torch.full((5, 8, chunk), float("nan"), device="cuda"), s, 0.1, sums_out=o, decay=decay, window=window,
+                        chunk_lens=i32(0, 0, 0, 0, 0) if chunk else None, err_flag=err)
+        assert int(err) == 0
+        for j, n in enumerate(lens):
+            assert torch.equal(o[j, :, :n], want[j, :, :n]) and torch.equal(o[j, :, n:], before[j, :, n:])
+
+
+def test_an_empty_chunk_flags_bad_lengths_and_pages(b):
+    kp = torch.randn(8, 2, 16, 128, device="cuda").bfloat16()
+    table = i32(*range(8)).view(4, 2).contiguous()
+    table[1, 1] = 99
+    sums = torch.ones(4, 2, 32, device="cuda")
+    out, err = torch.full_like(sums, 7.0), i32(0)
+    b.chunk_weights(torch.zeros(4, 0, 8, 128, device="cuda").bfloat16(), kp, table, i32(32, 20, 33, -1),
+                    torch.zeros(4, 8, 0, device="cuda"), sums, 0.1, sums_out=out, decay=0.25, err_flag=err)
+    assert int(err) == b.PKV_DEVERR_BAD_LEN | b.PKV_DEVERR_BAD_PAGE
+    assert bool((out[0] == 0.25).all()) and bool((out[1, :, :16] == 0.25).all()) and bool(out[1, :, 16:20].isnan().all())
+    assert bool((out[1, :, 20:] == 7.0).all()) and bool((out[2:] == 7.0).all())
