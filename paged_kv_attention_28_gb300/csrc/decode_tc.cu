@@ -1118,7 +1118,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           o[h] = __uint_as_float(r[h]);
-          if constexpr (LOGITS) o[h] += __uint_as_float(r[G + h]);
+          // (not to an infinite sum: the second part of a weight is often 0 or below it, and 0 x inf
+          // and inf - inf are NaN, where an infinite V makes the output infinite)
+          if constexpr (LOGITS) o[h] = fabsf(o[h]) < INFINITY ? o[h] + __uint_as_float(r[G + h]) : o[h];
           mh[h] = stats[(qb * NQ + h) * 2];
           lh[h] = stats[(qb * NQ + h) * 2 + 1];
         }

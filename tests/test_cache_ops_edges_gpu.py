@@ -4,6 +4,8 @@ values, results near the smallest numbers, more features than one kernel's grid 
 import pytest
 import torch
 
+from paged_kv_attention_28_gb300 import workloads
+
 pytestmark = pytest.mark.gpu
 
 
@@ -79,3 +81,34 @@ def test_an_empty_chunk_flags_bad_lengths_and_pages(b):
     assert int(err) == b.PKV_DEVERR_BAD_LEN | b.PKV_DEVERR_BAD_PAGE
     assert bool((out[0] == 0.25).all()) and bool((out[1, :, :16] == 0.25).all()) and bool(out[1, :, 16:20].isnan().all())
     assert bool((out[1, :, 20:] == 7.0).all()) and bool((out[2:] == 7.0).all())
+
+
+# ------------------------------------------------------------------------------------ decode with weights
+
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (16, 2, 128), (8, 8, 128), (8, 4, 64)])
+def test_infinite_values_reach_the_output_as_infinities(b, hq, hkv, d, splits):
+    """An infinite element of V makes its output element infinite, as the plain decode does, since every weight is
+    above 0; of both signs, or a NaN, it makes it NaN. The other elements and the sums do not change."""
+    lens = [200, 40]
+    c = workloads.make_paged_decode(31, 2, hq, hkv, d, 16, lens, num_pages=20, dtype="bf16")
+    dev = [t.cuda() for t in (c.q, c.k_pages, c.v_pages, c.block_table, c.kv_lens)]
+    sums = torch.zeros(2, hkv, c.block_table.shape[1] * 16, device="cuda")
+    clean, _, s0 = b.decode_paged_weights(*dev, sums.clone(), c.scale, num_splits=splits)
+    at = [(int(t), int(e)) for t, e in zip(torch.arange(0, 200, 3), torch.arange(200) % (d - 5))]  # (token, element) of sequence 0
+    want = clean.clone()
+    for t, e in at:
+        dev[2][int(c.block_table[0, t // 16]), :, t % 16, e] = float("inf")
+        want[0, :, e] = float("inf")
+    page = lambda t: int(c.block_table[1, t // 16])  # noqa: E731
+    inf = float("inf")
+    for t, e, x in ((0, 0, -inf), (39, 1, -inf), (5, 2, inf), (20, 2, -inf), (7, d - 1, float("nan"))):
+        dev[2][page(t), :, t % 16, e] = x
+        want[1, :, e] = x if e < 2 else float("nan")
+    got, _, s1 = b.decode_paged_weights(*dev, sums.clone(), c.scale, num_splits=splits)
+    plain, _ = b.decode_paged(*dev, c.scale, num_splits=splits)
+    assert torch.equal(s0, s1)
+    for y in (got, plain):
+        assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.isinf(), want.isinf())
+        assert torch.equal(y[want.isinf()], want[want.isinf()])
+    assert torch.equal(got[want.isfinite()], want[want.isfinite()])
