@@ -5,8 +5,8 @@ take less time than that, through the CPython module ``_pycall`` (csrc/pycall.cp
 pointers, checks shapes and dtypes on the host, and passes the current CUDA
 stream, or ``stream`` (a torch stream, or an object with its ``cuda_stream`` handle), which also owns the
 buffers that the call makes for itself. Every step of the computation runs in the library's kernels. If the
-library is missing, importing this module raises; nothing falls back to
-another implementation.
+library is missing, importing this module raises; if ``_pycall`` is, or was built for another PyTorch, the
+calls through it do. Nothing falls back to another implementation.
 """
 from __future__ import annotations
 
@@ -112,12 +112,30 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
-# The checks and calls of the operators whose small calls are bound by the host (csrc/pycall.cpp).
-from . import _pycall  # noqa: E402  (needs the library)
+class _Unavailable:
+    """Stands for the module where it cannot be used: every call through it raises."""
 
-if _pycall.torch_version.split(".")[:2] != torch.__version__.split(".")[:2]:
-    raise ImportError(f"_pycall.so was built for PyTorch {_pycall.torch_version}, this is {torch.__version__}: "
-                      "build it again with `python -m paged_kv_attention_28_gb300.build --force`")
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} goes through _pycall.so, {self._why}: build it again with "
+                          "`python -m paged_kv_attention_28_gb300.build --force`")
+
+
+def _load_pycall():
+    try:
+        from . import _pycall  # (needs the library)
+    except ImportError as e:
+        return _Unavailable(f"which cannot be loaded ({e})")
+    if _pycall.torch_version.split(".")[:2] != torch.__version__.split(".")[:2]:
+        return _Unavailable(f"which was built for PyTorch {_pycall.torch_version}, this is {torch.__version__}")
+    return _pycall
+
+
+# The checks and calls of the operators whose small calls are bound by the host (csrc/pycall.cpp). The others
+# need the library alone, whatever PyTorch there is.
+_pycall = _load_pycall()
 
 
 def status_string(status: int) -> str:

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -23,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpkvattn.so")
 PYCALL = os.path.join(PKG, "_pycall.so")
+PYCALL_FOR = os.path.join(BUILD, "pycall_torch_version")  # the PyTorch that it was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -47,67 +49,111 @@ def _flags(verbose_ptxas: bool):
     return f
 
 
-def _needs_rebuild(srcs) -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PYCALL):
+def _older_than(path: str, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
+
+
+def _headers():
+    return [p for d in (CSRC, INCLUDE) for ext in ("*.cuh", "*.h") for p in glob.glob(os.path.join(d, ext))]
+
+
+def _library_is_stale(srcs) -> bool:
+    return _older_than(LIB, srcs + _headers())
+
+
+def _torch_version() -> str:
+    """PyTorch's version without importing it, "" where there is none."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return ""
+
+
+def _module_is_stale() -> bool:
+    """Also where it was built for another PyTorch: a tensor's layout is the version's."""
+    if _older_than(PYCALL, glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h"))):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
-    deps = srcs + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(p) > t for p in deps)
+    try:
+        with open(PYCALL_FOR) as f:
+            return f.read() != _torch_version()
+    except OSError:
+        return True
+
+
+def _run(cmd) -> str | None:
+    """None, or what the command said when it failed."""
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return f"{cmd[0]}: {e}"
+    return r.stdout + r.stderr + f"{cmd[0]} returned {r.returncode}" if r.returncode else None
+
+
+def _compile_module(obj: str) -> str | None:
+    try:
+        inc = os.path.join(os.path.dirname(torch_lib()), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    except (ImportError, RuntimeError) as e:
+        return str(e)
+    return _run([os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-I", INCLUDE, "-isystem", inc,
+                 "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+                 "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "pycall.cpp"), "-o", obj])
+
+
+def _link_module(obj: str) -> str | None:
+    tmp = PYCALL + ".tmp"
+    # PyTorch's libraries are those that the importing process has loaded: no run path for them
+    said = _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libpkvattn.so",
+                 "-Wl,-rpath,$ORIGIN", "-L", torch_lib(), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+    if said is None:
+        os.replace(tmp, PYCALL)
+        with open(PYCALL_FOR, "w") as f:
+            f.write(_torch_version())
+    return said
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False) -> str:
+    """Builds what is out of date. A library that cannot be built raises; a module that cannot says so on
+    stderr and leaves the calls that need it to raise: the others need the library alone."""
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    if not force and not _needs_rebuild(srcs):
+    library, module = force or _library_is_stale(srcs), force or _module_is_stale()
+    if not library and not module:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    cc = nvcc()
     flags = _flags(verbose_ptxas)
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [cc] + flags + ["-c", src, "-o", obj]
+        cmd = [nvcc()] + flags + ["-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    def compile_pycall():
-        inc = os.path.join(os.path.dirname(torch_lib()), "include")
-        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
-        src, obj = os.path.join(CSRC, "pycall.cpp"), os.path.join(BUILD, "pycall.cpp.o")
-        cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-I", INCLUDE, "-isystem", inc,
-               "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
-               "-isystem", sysconfig.get_paths()["include"], "-c", src, "-o", obj]
-        return src, obj, subprocess.run(cmd, capture_output=True, text=True)
-
+    module_obj = os.path.join(BUILD, "pycall.cpp.o")
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        module = ex.submit(compile_pycall)
-        results = list(ex.map(compile_one, srcs))
-        module = module.result()
+        said = ex.submit(_compile_module, module_obj) if module else None
+        results = list(ex.map(compile_one, srcs)) if library else []
+        said = said.result() if module else None
     failed = False
-    for src, _, r in results + [module]:
+    for src, _, r in results:
         if r.returncode != 0 or (verbose_ptxas and not quiet):
             sys.stderr.write(r.stdout + r.stderr)
         failed |= r.returncode != 0
     if failed:
-        raise RuntimeError("a compiler failed; see the messages above")
-    objs = [o for _, o, _ in results]
-    tmp = LIB + ".tmp"
-    cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("link failed")
-    os.replace(tmp, LIB)
-    tmp = PYCALL + ".tmp"
-    # PyTorch's libraries are those that the importing process has loaded: no run path for them
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, module[1], "-L", PKG, "-l:libpkvattn.so",
-           "-Wl,-rpath,$ORIGIN", "-L", torch_lib(), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("the Python module's build failed")
-    os.replace(tmp, PYCALL)
+        raise RuntimeError("nvcc failed; see the messages above")
+    if library:
+        tmp = LIB + ".tmp"
+        cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + [o for _, o, _ in results] + ["-cudart", "static"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link failed")
+        os.replace(tmp, LIB)
+    if module:
+        said = said if said is not None else _link_module(module_obj)
+        if said is not None:
+            if os.path.exists(PYCALL):
+                os.remove(PYCALL)
+            sys.stderr.write(f"{said}\n_pycall.so was not built: the calls that go through it will raise\n")
     if not quiet:
         print(f"built {LIB}")
     return LIB
