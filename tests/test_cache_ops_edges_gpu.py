@@ -1,6 +1,8 @@
 """Calls at the edge of what the operators around the paged attention take: empty and padded chunks, infinite
 values, results near the smallest numbers, more features than one kernel's grid holds, tables of many pages.
 """
+import math
+
 import pytest
 import torch
 
@@ -43,6 +45,27 @@ def test_linear_with_more_features_than_the_few_token_kernel_has_tiles(b, m, act
     # k products added in fp32 and the bias, one rounding each at most S; one rounding to bf16
     bar = (k + 2) * 2.0 ** -24 * size + 2.0 ** -8 * want.abs()
     assert bool(((got.double() - want).abs() <= bar).all())
+
+
+@pytest.mark.parametrize("m,k", [(3, 8), (3, 512), (90, 8)])  # the tiled kernel, that of few tokens, the tiled one
+def test_small_results_of_silu_and_gelu(b, m, k):
+    """Results of 1e-36 and less, which bf16 still holds. y / (1 + 2^t) with |t| <= 136: t is off by 2^-24 of itself
+    for each of at most five roundings (constants, y^2, fma, product), so 2^t by 136 * 5 * 2^-24 ln 2 < 2^-14 of
+    itself, numbers below fp32's smallest normal by 2^-16 more at 2^-133; then half a step of bf16, or of its
+    smallest numbers (2^-133)."""
+    y = torch.tensor([-60.0, -87.0, -87.5, -88.0, -88.5, -89.0, -90.0, -92.0, -1e-30, 1e-30, 90.0, 3e38, -3e38]).bfloat16()
+    z = torch.tensor([-8.0, -9.875, -9.9375, -10.0, -10.0625, -10.125, -1e-30, 1e-30, 11.0, 3e38, -3e38]).bfloat16()
+    for act, v in (("silu", y), ("gelu_tanh", z)):
+        x, w = torch.zeros(m, k).bfloat16(), torch.zeros(len(v), k).bfloat16()
+        x[:, 0] = 1.0
+        w[:, 0] = v
+        got = b.linear(x.cuda(), w.cuda(), activation=act).double().cpu()
+        d = [float(t) for t in v]
+        t = d if act == "silu" else [2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3) for a in d]
+        want = torch.tensor([a / (1 + math.exp(-s)) if s > -700 else 0.0 for a, s in zip(d, t)], dtype=torch.float64)
+        off = (got - want).abs()
+        bar = (2.0 ** -8 + 2.0 ** -14 + 2.0 ** -16) * want.abs() + 2.0 ** -134
+        assert bool((off <= bar).all()), (act, got[0], want)
 
 
 # ------------------------------------------------------------------------------------ weights over a chunk
