@@ -113,9 +113,10 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 // Grid (S, tiles): CTA (r, t) multiplies K slices [r * kc_per_cta, ...) of W tile t, and
 // the S CTAs of tile t form one cluster. Every thread reaches both cluster barriers on
 // every path: the mbarrier waits are bounded, and a failed one only marks the result.
-// EPI: every sum goes through bias, activation and residual before it is stored.
+// EPI: every sum goes through bias, activation and residual before it is stored. (Three CTAs per SM are what shared
+// memory holds; told so, the compiler takes more registers, and 8 x 4096 x 4096 9.8 us for 10.1.)
 template <int NP, bool EPI>
-__global__ void __launch_bounds__(FG_THREADS)
+__global__ void __launch_bounds__(FG_THREADS, EPI ? 3 : 0)
 flat_gemm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                  const FgArgs a) {
   using C = FgCfg<NP>;

@@ -68,6 +68,23 @@ def test_small_results_of_silu_and_gelu(b, m, k):
         assert bool((off <= bar).all()), (act, got[0], want)
 
 
+@pytest.mark.parametrize("m,k", [(3, 8), (3, 512), (90, 8)])
+def test_gelu_keeps_the_precision_of_small_results(b, m, k):
+    """y Phi(y) from -13.5, where bf16's smallest numbers are, to 20. exp(-y^2 / 2) has an argument of at most 92, off by
+    three roundings of 2^-24 each: 92 * 3 * 2^-24 < 2^-15 of the result, with the polynomial's 2^-20 less than 2^-14;
+    numbers below fp32's smallest normal by 2^-149 / 2^-137 more. Then half a step of bf16, or of its smallest."""
+    y = torch.cat((torch.arange(-13.5, 0, 0.125), torch.arange(0, 20, 0.25), torch.tensor([-1e-30, 1e-30, -3e-38, 0.01, -0.01,
+                   -20.0, 3e38, -3e38]))).bfloat16()
+    x, w = torch.zeros(m, k).bfloat16(), torch.zeros(len(y), k).bfloat16()
+    x[:, 0] = 1.0
+    w[:, 0] = y
+    got = b.linear(x.cuda(), w.cuda(), activation="gelu").double().cpu()
+    want = torch.tensor([0.5 * v * math.erfc(-v / math.sqrt(2)) for v in y.double().tolist()], dtype=torch.float64)
+    bar = (2.0 ** -8 + 2.0 ** -14 + 2.0 ** -12 * (want.abs() < 2.0 ** -126)) * want.abs() + 2.0 ** -134
+    off = (got - want).abs()
+    assert bool((off <= bar).all()), (y[(off > bar).any(0)], got[:, (off > bar).any(0)])
+
+
 # ------------------------------------------------------------------------------------ weights over a chunk
 
 @pytest.mark.parametrize("in_place,decay", [(True, 0.5), (False, 0.5), (False, 1.0), (True, 1.0)])
