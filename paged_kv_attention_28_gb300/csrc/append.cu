@@ -94,8 +94,11 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, int
   const int n = a.chunk_lens ? __ldg(a.chunk_lens + b) : a.chunk_len;
   const bool bad_n = n < 0 || n > a.chunk_len;
   const int end = min(first + per_cta, bad_n ? a.chunk_len : n);  // tokens [first, end)
-  if (first >= end) return;  // padding
   const bool bad_len = bad_n || len < 0 || (int64_t)len + n > (int64_t)a.max_blocks * kPage;
+  if (first >= end) {  // padding, perhaps all of the sequence: then nobody else would report its length
+    if (bad_len && first == 0 && tid == 0) set_err(a.err_flag, PKV_DEVERR_BAD_LEN);
+    return;
+  }
   const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
   const int64_t t0 = (int64_t)b * a.chunk_len;  // the sequence's first token
   auto page_of = [&](int i) { return bad_len ? -1 : __ldg(table + (len + i) / kPage); };

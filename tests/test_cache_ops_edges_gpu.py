@@ -85,6 +85,25 @@ def test_gelu_keeps_the_precision_of_small_results(b, m, k):
     assert bool((off <= bar).all()), (y[(off > bar).any(0)], got[:, (off > bar).any(0)])
 
 
+# ------------------------------------------------------------------------------------ cache write
+
+def test_append_flags_a_bad_length_without_new_tokens(b):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(4, 3, 4, 64, generator=g, device="cuda")
+    kp, vp = torch.zeros(9, 2, 16, 64, device="cuda"), torch.zeros(9, 2, 16, 64, device="cuda")
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)
+    out = torch.full_like(x, 7.0)
+    for lens, news, flag in (((0, 32, 5, 9), (0, 0, 0, 0), 0), ((0, 33, 5, 9), (0, 0, 0, 0), 2), ((0, 3, -1, 9), (0, 0, 0, 0), 2),
+                             ((0, 3, -1, 9), (0, 3, 0, 2), 2)):
+        err = i32(0)
+        b.qk_norm_rope_append(x, x[:, :, :2].contiguous(), x[:, :, 2:].contiguous(), kp, vp, table, i32(*lens),
+                              chunk_lens=i32(*news), out=out, err_flag=err)
+        assert int(err) == flag, (lens, news)
+        for j, n in enumerate(news):
+            assert torch.equal(out[j, :n], x[j, :n]) and bool((out[j, n:] == 7.0).all())
+        out.fill_(7.0)
+
+
 # ------------------------------------------------------------------------------------ weights over a chunk
 
 @pytest.mark.parametrize("in_place,decay", [(True, 0.5), (False, 0.5), (False, 1.0), (True, 1.0)])
