@@ -492,7 +492,8 @@ int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_
   if (n_qo_heads % n_kv_heads || !std::isfinite(scale) || !std::isfinite(decay)) return PKV_ERR_INVALID_ARG;
   if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
   if ((long)max_blocks_per_seq * page_size > 0x7fffffffL) return PKV_ERR_INVALID_ARG;
-  if (chunk_len > max_blocks_per_seq * page_size) return PKV_ERR_INVALID_ARG;
+  // (padding may be wider than the table; the tokens that count are checked on the device)
+  if (chunk_len > max_blocks_per_seq * page_size && !chunk_lens) return PKV_ERR_INVALID_ARG;
   if (batch == 0) return PKV_OK;
   // (without queries nothing is left but the decay, and of that nothing in place at 1)
   if (chunk_len == 0 && decay == 1.0f && sums_in == sums_out) return PKV_OK;

@@ -3,10 +3,13 @@ values, results near the smallest numbers, more features than one kernel's grid 
 """
 import math
 
+import numpy as np
 import pytest
 import torch
 
+import oracle
 from paged_kv_attention_28_gb300 import workloads
+from tests.test_chunk_weights_gpu import make as make_chunk
 
 pytestmark = pytest.mark.gpu
 
@@ -140,6 +143,38 @@ def test_an_empty_chunk_flags_bad_lengths_and_pages(b):
     assert int(err) == b.PKV_DEVERR_BAD_LEN | b.PKV_DEVERR_BAD_PAGE
     assert bool((out[0] == 0.25).all()) and bool((out[1, :, :16] == 0.25).all()) and bool(out[1, :, 16:20].isnan().all())
     assert bool((out[1, :, 20:] == 7.0).all()) and bool((out[2:] == 7.0).all())
+
+
+@pytest.mark.parametrize("prefix,n,pad,window", [([3, 0], [10, 16], 40, 0), ([0, 200], [30, 7], 600, 0), ([5, 9], [20, 0], 100, 8)])
+def test_a_chunk_padded_past_the_table(b, prefix, n, pad, window):
+    """Padding may be wider than the table; the new tokens that count fit."""
+    q, kp, table, pl, lse, sums, _ = make_chunk(11, prefix, max(n), 8, 2, n, extra=0)
+    B, hq, scale = len(prefix), 8, 128 ** -0.5
+    used = max(p + x for p, x in zip(prefix, n))
+    blocks = (used + 15) // 16
+    assert pad > blocks * 16
+    table, sums = table[:, :blocks].contiguous(), sums[:, :, :blocks * 16].contiguous()
+    qp = torch.full((B, pad, hq, 128), float("nan")).bfloat16()
+    qp[:, :max(n)] = q
+    lp = torch.full((B, hq, pad), float("nan"))
+    lp[:, :, :max(n)] = lse
+    err = i32(0)
+    got = b.chunk_weights(qp.cuda(), kp.cuda(), table.cuda(), pl.cuda(), lp.cuda(), sums.cuda(), scale, window=window,
+                          chunk_lens=torch.tensor(n, dtype=torch.int32).cuda(), err_flag=err).cpu()
+    assert int(err) == 0
+    first = [max(0, x - window) if window else 0 for x in n]
+    w = oracle.key_weights(q.nan_to_num(0).double().numpy(), kp.double().numpy(), table.numpy(), pl.numpy(),
+                           lse.nan_to_num(0).double().numpy(), scale, first=first, last=n)
+    # a weight's logit is off by 2^-23 (128 S + 4 (S + |lse|)); n weights add n + 8 roundings; the old sum one more
+    S = scale * float(q.nan_to_num(0).double().abs().amax() * kp.nan_to_num(0).double().abs().sum(-1).amax())
+    e = 2.0 ** -23 * (128 * S + 4 * (S + float(lse.nan_to_num(0).abs().max())))
+    for j in range(B):
+        end = prefix[j] + n[j]
+        old = sums[j, :, :end].double().numpy()
+        want = w[j, :, :end] + old
+        bar = w[j, :, :end] * (2 * e + 2.0 ** -20 + (4 * max(n) + 8) * 2.0 ** -24) + (want + old) * 2.0 ** -23
+        assert (np.abs(got[j, :, :end].double().numpy() - want) <= bar).all()
+        assert torch.equal(got[j, :, end:], sums[j, :, end:])
 
 
 # ------------------------------------------------------------------------------------ decode with weights
