@@ -430,7 +430,8 @@ int attn_flat_gemm(const void* x, const void* w, void* y, int m, int n, int k, i
  *                  q; may be q itself when q_stride = n_qo_heads * head_dim, and must not overlap
  *                  another input or a pool (their addresses are refused). Padding rows are
  *                  left as they were
- *   k_pages, v_pages, block_table : the paged layout above (16-byte aligned pools)
+ *   k_pages, v_pages, block_table : the paged layout above (two pools, 16-byte aligned; one for both is
+ *                  refused)
  * A sequence with prefix_lens[b] < 0, chunk_lens[b] outside its range, or prefix_lens[b] +
  * chunk_lens[b] past the table sets PKV_DEVERR_BAD_LEN, a bad table entry
  * PKV_DEVERR_BAD_PAGE; the q_out rows of such tokens are NaN and their K and V are not
@@ -526,7 +527,7 @@ int attn_chunk_weights(const void* q, const void* k_pages, const int32_t* block_
  *   new_lens        : int32 [batch], out: min(n, budget)
  *   new_sums        : fp32 [batch][n_kv_heads][new_max_blocks * page_size], out: the kept
  *                     tokens' sums, 0 at and past the new length
- * Outputs must not overlap inputs (the same address is refused). A length < 0 or past the
+ * Outputs must not overlap inputs or one another (the same address is refused). A length < 0 or past the
  * table sets PKV_DEVERR_BAD_LEN and counts as 0. A bad entry of block_table sets
  * PKV_DEVERR_BAD_PAGE and makes the rows NaN; a bad entry of new_block_table sets it too and
  * its rows are not copied.

@@ -547,12 +547,17 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(sums)) return PKV_ERR_INVALID_ARG;
   // (a head's outputs are written while other heads still read the inputs)
-  if (new_lens == kv_lens || new_sums == sums || kept == block_table || kept == new_block_table)
-    return PKV_ERR_INVALID_ARG;
+  for (const void* out : {static_cast<const void*>(kept), static_cast<const void*>(new_lens), static_cast<const void*>(new_sums)})
+    for (const void* in : {static_cast<const void*>(k_pages), static_cast<const void*>(v_pages),
+                           static_cast<const void*>(block_table), static_cast<const void*>(kv_lens),
+                           static_cast<const void*>(sums), static_cast<const void*>(new_block_table)})
+      if (out == in) return PKV_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || page_size != 16) return PKV_ERR_UNSUPPORTED;
   if (batch > 65535 || n_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
   if ((long)max_blocks_per_seq * page_size > kMaxTokens || (long)new_max_blocks * page_size > kMaxTokens)
     return PKV_ERR_UNSUPPORTED;
+  if (kept == new_lens || static_cast<void*>(kept) == new_sums || static_cast<void*>(new_lens) == new_sums)
+    return PKV_ERR_INVALID_ARG;
   EvictArgs a{k_pages, v_pages, block_table, kv_lens, sums, new_block_table, kept, new_lens, new_sums, batch,
               max_blocks_per_seq, new_max_blocks, num_pages, n_kv_heads, head_dim, page_size, budget, n_sink,
               n_recent, dtype, err_flag};
@@ -584,8 +589,12 @@ int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_
   const int64_t qw = (int64_t)n_qo_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
   if (q_stride < qw || k_stride < kw || v_stride < kw) return PKV_ERR_INVALID_ARG;
   if (q_stride % 4 || k_stride % 4 || v_stride % 4) return PKV_ERR_INVALID_ARG;
-  if ((q_out == q && q_stride != qw) || q_out == k || q_out == v || q_out == k_pages || q_out == v_pages)
-    return PKV_ERR_INVALID_ARG;
+  if (q_out == q && q_stride != qw) return PKV_ERR_INVALID_ARG;
+  for (const void* p : {k, v, static_cast<const void*>(k_pages), static_cast<const void*>(v_pages), q_norm, k_norm,
+                        static_cast<const void*>(inv_freq), static_cast<const void*>(positions),
+                        static_cast<const void*>(pair_axis), static_cast<const void*>(block_table),
+                        static_cast<const void*>(prefix_lens), static_cast<const void*>(chunk_lens)})
+    if (q_out == p) return PKV_ERR_INVALID_ARG;
   const uintptr_t quad = dtype == PKV_F32 ? 16 : 8;
   for (const void* p : {q, k, v, q_norm, k_norm, static_cast<const void*>(q_out)})
     if (reinterpret_cast<uintptr_t>(p) % quad) return PKV_ERR_INVALID_ARG;
@@ -594,6 +603,7 @@ int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_
     return PKV_ERR_UNSUPPORTED;
   if (batch > 65535 || n_qo_heads > (1 << 20) || n_kv_heads > (1 << 20))
     return PKV_ERR_UNSUPPORTED;
+  if (k_pages == v_pages) return PKV_ERR_INVALID_ARG;  // a token's key and value would share a slot
   AppendArgs a{q, k, v, q_stride, k_stride, v_stride, q_norm, k_norm, norm_eps, inv_freq, rotary_dim,
                interleaved, positions, n_axes, pair_axis, block_table, prefix_lens, chunk_lens, q_out,
                k_pages, v_pages, batch, chunk_len, max_blocks_per_seq, num_pages, n_qo_heads, n_kv_heads,

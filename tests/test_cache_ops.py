@@ -100,6 +100,16 @@ def test_append_refuses(b, bad, want):
     assert b.lib.attn_qk_norm_rope_append(*append_args(b, **bad)) == want
 
 
+@pytest.mark.parametrize("name", ["k", "v", "qn", "kn", "fr", "pos", "pa", "bt", "pl", "cl", "kp", "vp"])
+def test_append_refuses_an_output_at_an_input(b, name):
+    other = dict(vp=P3) if name != "vp" else dict(kp=P3)
+    assert b.lib.attn_qk_norm_rope_append(*append_args(b, **{name: P2, **other})) == -1
+
+
+def test_append_refuses_one_pool_for_keys_and_values(b):
+    assert b.lib.attn_qk_norm_rope_append(*append_args(b)) == -1
+
+
 def weights_args(b, **kw):
     a = dict(q=P, kp=P, vp=P, bt=P, ln=P, out=P, lse=None, si=P, so=P, batch=1, mb=4, np=4, hq=8, hkv=2, d=128, page=16,
              scale=0.1, decay=1.0, splits=0, dt=b.PKV_BF16, ws=P, wsz=1 << 30)
@@ -146,6 +156,21 @@ def evict_args(b, **kw):
 ])
 def test_evict_refuses(b, bad, want):
     assert b.lib.attn_cache_evict(*evict_args(b, **bad)) == want
+
+
+@pytest.mark.parametrize("out", ["kept", "nl", "ns"])
+@pytest.mark.parametrize("name", ["kp", "vp", "bt", "ln", "s", "nt"])
+def test_evict_refuses_an_output_at_an_input(b, out, name):
+    own = dict(kept=ctypes.c_void_p(1 << 23), nl=ctypes.c_void_p(1 << 24), ns=ctypes.c_void_p(1 << 25), **{name: P2})
+    own[out] = P2
+    assert b.lib.attn_cache_evict(*evict_args(b, **own)) == -1
+
+
+@pytest.mark.parametrize("one,two", [("kept", "nl"), ("kept", "ns"), ("nl", "ns")])
+def test_evict_refuses_two_outputs_at_one_address(b, one, two):
+    own = dict(kept=ctypes.c_void_p(1 << 23), nl=ctypes.c_void_p(1 << 24), ns=ctypes.c_void_p(1 << 25))
+    own[one] = own[two]
+    assert b.lib.attn_cache_evict(*evict_args(b, **own)) == -1
 
 
 def chunk_args(b, **kw):
