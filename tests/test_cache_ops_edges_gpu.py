@@ -10,6 +10,7 @@ import torch
 import oracle
 from paged_kv_attention_28_gb300 import workloads
 from tests.test_chunk_weights_gpu import make as make_chunk
+from tests.test_weights_evict_gpu import check_evict
 
 pytestmark = pytest.mark.gpu
 
@@ -206,3 +207,31 @@ def test_infinite_values_reach_the_output_as_infinities(b, hq, hkv, d, splits):
         assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.isinf(), want.isinf())
         assert torch.equal(y[want.isinf()], want[want.isinf()])
     assert torch.equal(got[want.isfinite()], want[want.isfinite()])
+
+
+# ------------------------------------------------------------------------------------ eviction
+
+@pytest.mark.parametrize("kind", ["mixed", "equal", "odd", "close"])
+@pytest.mark.parametrize("lens,budget,sink,recent,blocks", [
+    ([53249, 30], 4000, 4, 64, None), ([60001], 59990, 0, 1, None), ([70000, 65536], 1, 0, 0, None),
+    ([2000, 1, 0, 57], 56, 2, 9, 3400), ([66000], 300, 150, 150, None),
+])
+def test_evict_from_tables_past_the_rows_kept_in_shared_memory(b, kind, lens, budget, sink, recent, blocks):
+    """Rows of more than 53248 tokens, and short sequences in tables that could hold as many."""
+    check_evict(b, lens, 1, 64, "bf16", budget, sink, recent, kind=kind, blocks=blocks)
+
+
+def test_evict_reads_no_further_than_the_length_in_a_wide_table(b):
+    n, blocks, budget = 1500, 4000, 100
+    g = torch.Generator().manual_seed(3)
+    order = torch.randperm(110, generator=g).to(torch.int32)
+    table = torch.full((1, blocks), -1, dtype=torch.int32)
+    table[0, :94] = order[:94]
+    s = torch.full((1, 1, blocks * 16), float("nan"))
+    s[0, 0, :n] = torch.rand(n, generator=g)
+    kp = torch.randn(110, 1, 16, 64, generator=g).cuda()
+    err = i32(0)
+    kept, nl, _ = b.cache_evict(kp, kp.clone(), table.cuda(), i32(n), s.cuda(), order[94:101].view(1, 7).cuda(), budget, 1, 4,
+                                err_flag=err)
+    wk, _, _ = oracle.evict([n], s.numpy(), budget, 1, 4)
+    assert int(err) == 0 and int(nl) == budget and kept[0, 0].tolist() == wk[0]
