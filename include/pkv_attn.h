@@ -271,6 +271,8 @@ int attn_decode_paged_fp8(const void* q, const void* k_pages, const void* v_page
  * token i attends to keys 0 .. prefix_lens[b] + i of its own sequence (the causal mask
  * with an offset), read through the block table ("快速注意力内核与算子融合", Q&A on
  * paged attention and on FlashAttention; the pages do not describe the combination).
+ * The V of a masked key enters a query's product with weight 0, so all of those slots must
+ * hold finite values, also where a shorter chunk is padded to chunk_len.
  *
  *   q, out      : bf16 [batch][chunk_len][n_qo_heads][head_dim], contiguous
  *   k_pages, v_pages, block_table : the paged layout above (bf16 pools)
@@ -426,6 +428,11 @@ int attn_flat_gemm(const void* x, const void* w, void* y, int m, int n, int k, i
  *                  outside the range sets PKV_DEVERR_BAD_AXIS and makes its pair NaN
  *   chunk_lens   : int32 [batch], new tokens of each sequence (0 .. chunk_len), the rest of
  *                  its row being padding; NULL: chunk_len each
+ *                  (attn_prefill_paged_chunk takes none: for ragged chunks its padding queries
+ *                  read the slots behind a sequence, up to prefix_lens[b] + chunk_len, which this
+ *                  call leaves as they were. The table needs pages for them and they must hold
+ *                  finite values, as in a pool that was zeroed when it was made; the rows of the
+ *                  queries that count then do not depend on them. A NaN there reaches those rows)
  *   q_out        : dtype [batch][chunk_len][n_qo_heads][head_dim], contiguous, aligned like
  *                  q; may be q itself when q_stride = n_qo_heads * head_dim, and must not overlap
  *                  another input or a pool (their addresses are refused). Padding rows are

@@ -328,8 +328,9 @@ def prefill_paged_chunk(q, k_pages, v_pages, block_table, prefix_lens, scale, ou
                         err_flag=None, stream=None):
     """Chunked prefill over the paged cache through ``attn_prefill_paged_chunk``.
 
-    ``q`` ``[B, C, Hq, D]``; the new tokens' K/V are already in the pools. Returns
-    ``(out, lse)`` with ``lse`` ``[B, Hq, C]``."""
+    ``q`` ``[B, C, Hq, D]``; the new tokens' K/V are already in the pools. Where a chunk is padded, the slots
+    of its padding must be in the table and hold finite values. Returns ``(out, lse)`` with ``lse``
+    ``[B, Hq, C]``."""
     B, C, Hq, D = q.shape
     num_pages, Hkv, P, D2 = k_pages.shape
     assert D2 == D

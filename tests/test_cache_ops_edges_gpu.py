@@ -178,6 +178,37 @@ def test_a_chunk_padded_past_the_table(b, prefix, n, pad, window):
         assert torch.equal(got[j, :, end:], sums[j, :, end:])
 
 
+def test_unwritten_slots_of_a_padded_chunk_may_hold_any_finite_value(b):
+    """Cache write and chunked prefill of ragged chunks: the prefill's padding queries read the slots behind a
+    sequence, which the cache write has left as they were. The queries that count come out the same,
+    bit for bit, whatever finite values are there."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    B, C, hq, hkv, n, prefix = 3, 90, 8, 2, (90, 1, 61), i32(0, 37, 100)
+    x = torch.randn(B, C, hq + 2 * hkv, 128, generator=g, device="cuda").bfloat16()
+    table = torch.randperm(60, generator=g, device="cuda")[:36].to(torch.int32).view(B, 12).contiguous()
+    old = torch.randn(60, hkv, 16, 128, generator=g, device="cuda").bfloat16()
+    got = []
+    for junk in (0.0, 1.0, 1e30, -3e38):
+        kp, vp = (torch.full((60, hkv, 16, 128), junk, device="cuda").bfloat16() for _ in range(2))
+        for j in range(B):  # the prefix's tokens
+            for t in range(int(prefix[j])):
+                p = int(table[j, t // 16])
+                kp[p, :, t % 16], vp[p, :, t % 16] = old[p, :, t % 16], old[p, :, 15 - t % 16]
+        q = b.qk_norm_rope_append(x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:], kp, vp, table, prefix,
+                                  chunk_lens=i32(*n), out=torch.zeros(B, C, hq, 128, device="cuda").bfloat16())
+        err = i32(0)
+        out, lse = b.prefill_paged_chunk(q, kp, vp, table, prefix, 128 ** -0.5, err_flag=err)
+        s = b.chunk_weights(q, kp, table, prefix, lse, torch.zeros(B, hkv, 192, device="cuda"), 128 ** -0.5,
+                            chunk_lens=i32(*n), err_flag=err)
+        assert int(err) == 0
+        got.append([out[j, :n[j]] for j in range(B)] + [lse[j, :, :n[j]] for j in range(B)] + [s])
+    for other in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], other))
+    assert all(bool(t.isfinite().all()) for t in got[0])
+    count = torch.tensor([hq // hkv * float(x) for x in n], device="cuda")
+    assert bool(((got[0][-1].sum(-1) - count[:, None]).abs() < 1e-3 * count[:, None]).all())
+
+
 # ------------------------------------------------------------------------------------ decode with weights
 
 @pytest.mark.parametrize("splits", [1, 3])
