@@ -17,42 +17,10 @@ struct Epilogue {
   int activation;
 };
 
-// Two fp32 values in a register pair, for the two-wide multiplies and fused multiply-adds.
-using Two = uint64_t;
-__device__ __forceinline__ Two two(float x, float y) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void split(Two v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 __device__ __forceinline__ float rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-
-// y / (1 + 2^(2 t)) for two values, with h = 2^-|t|: y / (1 + h^2) for t <= 0 and y h^2 / (1 + h^2) above, which keeps
-// the relative precision of small results. (A quotient by a divisor past 2^126 comes back as 0, which for
-// silu is at y = -87.3, where the result is still 1e-36.) h stays a normal number where h^2 is none.
-// The quotient for every y is 1 % faster (2611 x 11008 x 256 with silu 35.3 for 35.6 us); one value at a time 4 % slower.
-__device__ __forceinline__ void over_one_plus_exp4(float& y0, float& y1, Two t) {
-  float t0, t1, d0, d1, s0, s1;
-  split(t, t0, t1);
-  const Two y = two(y0, y1), h = two(ex2(-fabsf(t0)), ex2(-fabsf(t1)));
-  split(fma2(h, h, two(1.0f, 1.0f)), d0, d1);
-  split(mul2(mul2(y, h), h), s0, s1);
-  split(mul2(two(t0 > 0.0f ? s0 : y0, t1 > 0.0f ? s1 : y1), two(rcp(d0), rcp(d1))), y0, y1);
 }
 
 // gelu(y) = y Phi(y), Phi the normal distribution. With a = |y| and q = Phi(-a) it is y q below 0 and y (1 - q) above:
@@ -61,7 +29,7 @@ __device__ __forceinline__ void over_one_plus_exp4(float& y0, float& y1, Two t) 
 // degree 8 that is nearest to Phi(-a) exp(a^2 / 2) for 0 <= a <= 14.5 (a weighted least-squares fit on Chebyshev
 // nodes of s, reweighted until its relative errors are even: 6e-8). In fp32 the result is off by
 // 2^-22 |y| and by 2^-17 of itself, more only below fp32's smallest normal number. 2611 x 11008 x 256: 61 us with
-// erff, 47 with this, 48 where it takes two values at a time.
+// erff, 49 with this.
 __device__ __forceinline__ float gelu(float y) {
   constexpr float kP[9] = {0x1.eec024p-18f, 0x1.e96848p-4f, 0x1.f37ce0p-4f, 0x1.836c7ep-4f, 0x1.246216p-3f,
                            -0x1.3abc1cp-4f, 0x1.d4e49cp-3f, -0x1.5abddap-3f, 0x1.3aa222p-5f};
@@ -74,32 +42,36 @@ __device__ __forceinline__ float gelu(float y) {
 }
 
 // gelu_tanh(y) = y/2 (1 + tanh u) = y sigmoid(2u), u = sqrt(2/pi) (y + 0.044715 y^3), and silu(y) =
-// y sigmoid(y), the sigmoids as 1 / (1 + 2^(2 t)).
+// y sigmoid(y). sigmoid = 1 / (1 + 2^t) keeps the relative precision of small results, but a reciprocal of a number
+// past 2^126 comes back as 0, which for silu is at y = -87.3, where the result is still 1e-36. With the
+// divisor scaled by 2^-16 that is at t = 142, past bf16's smallest numbers. 4096 x 11008 x 4096 takes the same time
+// as with y / (1 + 2^t), 2611 x 11008 x 256 with silu 35.9 us for 35.0.
+__device__ __forceinline__ float times_sigmoid(float y, float t16) {  // t - 16
+  return y * (rcp(ex2(t16) + 0x1p-16f) * 0x1p-16f);
+}
+
 template <int ACT>
-__device__ __forceinline__ void activate(float& y0, float& y1) {
-  constexpr float kL = 1.4426950408889634f, kU = kL * 0.7978845608028654f;  // log2 e, and times sqrt(2/pi)
+__device__ __forceinline__ float activate(float y) {
   if constexpr (ACT == PKV_ACT_RELU) {  // NaN stays
-    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(y0));
-    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(y1));
-  } else if constexpr (ACT == PKV_ACT_GELU) {
-    y0 = gelu(y0);
-    y1 = gelu(y1);
-  } else if constexpr (ACT == PKV_ACT_GELU_TANH) {
-    const Two y = two(y0, y1);
-    over_one_plus_exp4(y0, y1, mul2(y, fma2(mul2(y, y), two(-kU * 0.044715f, -kU * 0.044715f), two(-kU, -kU))));
-  } else if constexpr (ACT == PKV_ACT_SILU) {
-    over_one_plus_exp4(y0, y1, mul2(two(y0, y1), two(-0.5f * kL, -0.5f * kL)));
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(y));
+    return r;
   }
+  constexpr float kL = 1.4426950408889634f, kU = kL * 2.0f * 0.7978845608028654f;  // log2 e, and times 2 sqrt(2/pi)
+  if constexpr (ACT == PKV_ACT_GELU) return gelu(y);
+  if constexpr (ACT == PKV_ACT_GELU_TANH)
+    return times_sigmoid(y, fmaf(y, fmaf(y * y, -kU * 0.044715f, -kU), -16.0f));
+  if constexpr (ACT == PKV_ACT_SILU) return times_sigmoid(y, fmaf(y, -kL, -16.0f));
+  return y;
 }
 
 // y[i] = act(y[i]) for N values; the choice is uniform, so it is made once per call.
 template <int N>
 __device__ __forceinline__ void activate_all(float (&y)[N], int act) {
-  static_assert(N % 2 == 0, "pairs");
-#define PKV_ACT_CASE(A)                                                                    \
-  case A: {                                                                                \
-    _Pragma("unroll") for (int i = 0; i < N; i += 2) activate<A>(y[i], y[i + 1]);          \
-    break;                                                                                 \
+#define PKV_ACT_CASE(A)                                    \
+  case A: {                                                \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) y[i] = activate<A>(y[i]); \
+    break;                                                 \
   }
   switch (act) {
     PKV_ACT_CASE(PKV_ACT_RELU)
