@@ -454,14 +454,21 @@ constexpr int kWide = 224;  // tiles from this width take one block per stage
 }  // namespace
 
 int launch_linear(const LinearArgs& p, cudaStream_t stream) {
-  // Few tokens stream the weights (flat_gemm.cu) where that is most of the time. Its reduction over a
-  // cluster and its epilogue, which grows with the tokens, cost more than a tile here for short products,
-  // and past 32 tokens for all but long ones. There and here, in us: 8 x 1024 x 72 5.8 and 5.2, 40 x 1024 x 72
-  // 11.6 and 4.9, 64 x 4096 x 512 10.5 and 6.8, 64 x 11008 x 1024 14.6 and 9.0; but 8 x 1024 x 1024 5.5 and 7.3,
-  // 32 x 4096 x 4096 11 and 13, 64 x 4096 x 4096 with cold weights 21 and 25, 64 x 1024 x 8192 12.6 and 19.5.
+  // Few tokens stream the weights (flat_gemm.cu) where that is most of the time. Where its plan splits K over a
+  // cluster, that and its epilogue, which grows with the tokens, cost more than a tile here for short products, and
+  // past 32 tokens for all but long ones. There and here, in us, weights cold: 8 x 1024 x 72 5.8 and 5.2; 64 tokens,
+  // 4096 x 512 9.5 and 6.8, 11008 x 1024 14.3 and 10.5, 12288 x 2048 17.8 and 15.8, 8192 x 4096 27 and 21; but 8 x 1024 x
+  // 1024 5.5 and 7.0, 32 x 4096 x 4096 11 and 17, 64 x 4096 x 4096 13 and 17, 64 x 1024 x 8192 12 and 28. Without a split
+  // (k up to 64, or more tiles than the SMs take at once) it is ahead everywhere: 16 x 22016 x 64 3.8 and 8.1, 64 x 4096
+  // x 64 4.1 and 5.2, 64 x 32000 x 1024 14 and 17, x 4096 45 and 50. Over 7 token counts up to 64, 16 n from 256 to 32000 and
+  // 9 k from 64 to 8192 the rule is 1 % off the better of the two on average, up to 43 % at single sizes (32 x 6144 x 1024, 13.4
+  // there for 9.4: 48 tiles by 6 do not fit the SMs at once; 33 x 12288 x 6144, 35 here for 29).
   // More features than the flat kernel's grid holds run here whatever their time.
-  const bool tiled = p.k <= 128 || (p.m > 32 && (p.k <= 1024 || p.k <= p.n / 2)) || p.n > kFlatGemmMaxN;
-  if (p.m <= kFlatGemmMaxM && !tiled) return launch_flat_linear(p, stream);
+  if (p.m <= kFlatGemmMaxM && p.n <= kFlatGemmMaxN) {
+    const bool tiled = plan_flat_gemm(p.m, p.n, p.k).splits > 1 &&
+                       (p.k <= 128 || (p.m > 32 && (p.k <= 1024 || p.k <= p.n / 2)));
+    if (!tiled) return launch_flat_linear(p, stream);
+  }
   if (p.m > 0x7fffff00 || p.n > 0x7fffff00) return PKV_ERR_UNSUPPORTED;  // (tile ends fit 32 bits)
   int sms = device_sm_count();
   if (sms <= 1) sms = 148;
