@@ -94,6 +94,8 @@ extern "C" {
  *                      chunked prefill: PKV_BF16, head_dim 128, page_size 16, groups dividing 128
  *   linear           : PKV_BF16; any m and n; k a multiple of 8
  *   accumulated weights over a chunk, eviction : up to 2^30 tokens per sequence
+ *   append, accumulated weights of a step, eviction : batch up to 65535; KV heads up to 65535
+ *                      (append: 2^20); over a chunk batch times KV heads below 2^30
  */
 
 /* Human-readable name of a status code. Static storage; never NULL. */
@@ -470,7 +472,8 @@ int attn_qk_norm_rope_append(const void* q, const void* k, const void* v, int64_
  * the newest token must have been set (to 0) before. sums_out may be sums_in (in place), and
  * must not overlap it otherwise. decay is finite (1: plain accumulation). out, lse, splits and
  * errors are as for attn_decode_paged (out is closer to the exact value than that call's where
- * the tensor cores take the weights: two bf16 parts of each, not one); a row that came out
+ * the tensor cores take the weights: two bf16 parts of each, 2^-17 of the weight, not one; infinite V
+ * makes infinite out, as there); a row that came out
  * NaN makes its group's sums NaN, and a bad length leaves the sequence's sums as they were. workspace: at least
  * attn_decode_weights_workspace_size bytes, 256-byte aligned: the split partials, the call's
  * logits (fp32 [batch][n_qo_heads][max_blocks_per_seq * page_size]) and log-sum-exps.
@@ -558,8 +561,9 @@ int attn_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table,
  * The product accumulates in fp32; bias, activation and residual are applied in fp32 and the
  * result is rounded once. k >= 1 a multiple of 8. m = 0 or n = 0 does nothing. err_flag
  * (nullable) gets PKV_DEVERR_TIMEOUT if a bounded wait gave up; the outputs affected are NaN.
- * Few tokens (at most 64) run as attn_flat_gemm does where the weights' stream is most of the
- * time, the rest on a tiled kernel.
+ * Small results keep their relative precision, down to the smallest numbers of bf16. Few tokens
+ * (at most 64) run as attn_flat_gemm does where the weights' stream is most of the time, the rest
+ * on a tiled kernel.
  */
 int attn_linear(const void* x, const void* w, const void* bias, const void* residual, void* y,
                 int m, int n, int k, int activation, int dtype, int32_t* err_flag, void* stream);

@@ -10,13 +10,14 @@
 // products run.
 //
 // Bound: the tensor cores, 2 m n k operations; for few tokens the weights' bytes. 4096 x 11008 x 4096 with
-// bias and gelu takes 195 us in a burst (1.9 PFLOP/s, the rate of the library's plain product; the tensor
-// pipe is busy 91 % of the time) and 228 us under the power limit. BN is the multiple of 32 for which the
+// bias and gelu_tanh takes 195 to 200 us in a burst (1.9 PFLOP/s, the rate of the library's plain product; the tensor
+// pipe is busy 91 % of the time) and 225 to 229 us under the power limit. BN is the multiple of 32 for which the
 // rounds of tiles over the pairs take least (choose_width); what is lost is the last round: 1024 x 4096
 // x 4096 takes 24 us where its products are 18. A short product is bound by its epilogue, whose loads
-// are a chain: 2611 x 11008 x 256 takes 28 us, 50 with a residual (46 and 77 with four warps that ask for
+// are a chain: 2611 x 11008 x 256 takes 27 us, 45 to 49 with a residual (46 and 77 with four warps that ask for
 // everything when they need it), of which the products with their operands from the L2 are 17. Rows
-// that no 16-byte store fits go through shared memory (1152 x 4097 x 1024 with residual: 75 to 31 us). Not
+// that no 16-byte store fits go through shared memory (1152 x 4097 x 1024 with residual: 75 to 31 us, 40 where the
+// tensors are not in the L2). Not
 // kept: sixteen warps (no faster, small products 3 % slower), y through shared memory and TMA (the same
 // time where rows are aligned to 32 bytes).
 #include <cuda.h>
@@ -188,7 +189,9 @@ __device__ __forceinline__ void commit_pair(uint32_t mbar) {
       : "memory");
 }
 // Arrives on a barrier of the pair's first CTA. Relaxed: what it announces is that reads of tensor memory
-// are over, which tcgen05.wait::ld has seen to; a release would wait for the tile's stores as well.
+// are over. tcgen05.wait::ld and the fence before this order the arriving lane's, the __syncwarp between
+// them the other lanes', and the issuer's fence after its wait orders the products behind them. A release
+// would wait for the tile's stores as well.
 __device__ __forceinline__ void arrive_remote(uint32_t mbar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
