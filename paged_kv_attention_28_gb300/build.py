@@ -69,9 +69,13 @@ def _torch_version() -> str:
         return ""
 
 
+def _module_is_older_than_its_sources() -> bool:
+    return _older_than(PYCALL, glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
 def _module_is_stale() -> bool:
     """Also where it was built for another PyTorch: a tensor's layout is the version's."""
-    if _older_than(PYCALL, glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h"))):
+    if _module_is_older_than_its_sources():
         return True
     try:
         with open(PYCALL_FOR) as f:
@@ -151,9 +155,10 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = False)
     if module:
         said = said if said is not None else _link_module(module_obj)
         if said is not None:
-            if os.path.exists(PYCALL):
+            # one that only may be for another PyTorch stays: the binding looks at what it was built for
+            if os.path.exists(PYCALL) and _module_is_older_than_its_sources():
                 os.remove(PYCALL)
-            sys.stderr.write(f"{said}\n_pycall.so was not built: the calls that go through it will raise\n")
+            sys.stderr.write(f"{said}\n_pycall.so was not built: without it the calls that go through it raise\n")
     if not quiet:
         print(f"built {LIB}")
     return LIB

@@ -81,8 +81,10 @@ def test_a_module_that_cannot_be_built_leaves_the_library(build, monkeypatch, tm
     monkeypatch.setattr(build, "BUILD", str(tmp_path))
     before = os.path.getmtime(build.LIB)
     for cxx in ("false", "/nonexistent/g++"):
-        module.write_text("an old one")
-        monkeypatch.setenv("CXX", cxx)
-        assert build.build(quiet=True) == build.LIB
-        assert "was not built" in capsys.readouterr().err
-        assert not module.exists() and os.path.getmtime(build.LIB) == before
+        for age in (10 ** 9, 0):
+            module.write_text("older than its sources, or of an unknown PyTorch")
+            os.utime(module, (os.path.getmtime(module) - age,) * 2)
+            monkeypatch.setenv("CXX", cxx)
+            assert build.build(quiet=True) == build.LIB
+            assert "was not built" in capsys.readouterr().err
+            assert module.exists() == (age == 0) and os.path.getmtime(build.LIB) == before
