@@ -7,7 +7,7 @@
 //   t   = position[axis of the pair] * inv_freq[pair]
 // in fp32, rounded once to the row's type. Every element is read once and written once, so
 // the call is bound by those bytes: 8192 tokens of 48 rows of 128 bf16, 201 MB, take 42 us, 4.8 TB/s, half of
-// them (the rest padding) 23 to 27 us; 64 tokens 3.4 us, a launch. 62 % of the issue slots are taken, at 8 bytes an
+// them (the rest padding) 22 to 30 us, by where the tensors lie in memory; 64 tokens 3.4 us, a launch. 62 % of the issue slots are taken, at 8 bytes an
 // access in bf16 and a norm weight loaded and widened for every row: that is this code's, not the work's. Not kept:
 // rows asked for two to four batches ahead through shared memory (1 to 15 % slower at twice the
 // warps, so it is not the loads' latency), two tokens at a time that share addresses and weights (7 %
