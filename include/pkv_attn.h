@@ -96,6 +96,8 @@ extern "C" {
  *   accumulated weights over a chunk, eviction : up to 2^30 tokens per sequence
  *   append, accumulated weights of a step, eviction : batch up to 65535; KV heads up to 65535
  *                      (append: 2^20); over a chunk batch times KV heads below 2^30
+ *   FP8 pages: attn_decode_paged_fp8 only. A page has one scale per KV head, so a token written to
+ *                      it, or gathered beside tokens of another page, would re-quantise the page
  */
 
 /* Human-readable name of a status code. Static storage; never NULL. */
