@@ -302,8 +302,8 @@ struct PagesArgs {
   int batch, max_blocks, num_pages, page_size;
   int32_t* err_flag;
   // workspace
-  int32_t *n_moves, *counts, *start, *from, *move_from, *move_to, *list;
-  uint32_t* key;
+  int32_t *n_moves, *counts, *start, *move_from, *move_to, *list;
+  uint32_t *key, *from;
 };
 // The workspace's size, and with `a` its parts.
 size_t pages_layout(PagesArgs* a, char* w, int batch, int num_pages);

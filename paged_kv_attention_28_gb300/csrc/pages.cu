@@ -79,7 +79,7 @@ struct Team {
   uint32_t* own_key;  // kShared: the same of this CTA, else key
   int32_t* counts;   // [3][kScanWarps]
   int32_t* start;    // [batch]: of each sequence among the wanted pages
-  int32_t* from;     // [batch]: its first wanted entry, times 2, and whether that is a copy
+  uint32_t* from;    // [batch]: its first wanted entry, times 2, and whether that is a copy (all 32 bits: pages of one token)
   int32_t* hole;     // compaction: [num_pages / 2], free pages among the first ones
   int32_t* list;     // reservation, kSpread: the free pages that are wanted, in order
   uint16_t* small_list;  // the same, not kSpread (kSmallPages fit 16 bits; in hole's place)
@@ -145,8 +145,8 @@ __device__ __forceinline__ Team<M> team_of(const PagesArgs& a) {
     t.counts = at;
     t.moves = at + 3 * kWarps;
     t.start = t.moves + 1;
-    t.from = t.start + a.batch;
-    t.middle = t.from + a.batch;
+    t.from = reinterpret_cast<uint32_t*>(t.start + a.batch);
+    t.middle = t.start + 2 * a.batch;
     t.seq = smem + (t.middle + a.batch - at);
     t.key = reinterpret_cast<uint32_t*>(t.middle + 3 * a.batch);
     t.hole = reinterpret_cast<int32_t*>(t.key + a.num_pages);
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesArgs a)
       const int y = __shfl_up_sync(0xffffffffu, x, off);
       if (lane >= off) x += y;
     }
-    if (b < b_hi) t.start[b] = wanted + x - own, t.from[b] = 2 * w.from + w.copy;
+    if (b < b_hi) t.start[b] = wanted + x - own, t.from[b] = 2u * (uint32_t)w.from + w.copy;
     wanted += __shfl_sync(0xffffffffu, x, 31);
   }
   t.set_count(1, seq_run, wanted);
@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1) reserve_kernel(const PagesArgs a)
       else n = half;
     }
     const int p = M == kSpread ? t.get(t.list + r) : t.small_list[r];
-    const int from = t.get(t.from + b), i = r - t.get(t.start + b);
+    const uint32_t from = t.get(t.from + b);
+    const int i = r - t.get(t.start + b);
     const int64_t at = (int64_t)b * a.max_blocks + (from >> 1) + i;
     if (i == 0 && (from & 1)) {
       const int m = atomicAdd(t.moves, 1);
@@ -502,7 +503,7 @@ size_t pages_layout(PagesArgs* a, char* w, int batch, int num_pages) {
     a->move_from = reinterpret_cast<int32_t*>(w + head + pages);
     a->move_to = reinterpret_cast<int32_t*>(w + head + pages + moves);
     a->start = reinterpret_cast<int32_t*>(w + head + pages + 2 * moves);
-    a->from = reinterpret_cast<int32_t*>(w + head + pages + 2 * moves + seqs);
+    a->from = reinterpret_cast<uint32_t*>(w + head + pages + 2 * moves + seqs);
     a->list = reinterpret_cast<int32_t*>(w + head + pages + 2 * moves + 2 * seqs);
   }
   return head + 2 * pages + 2 * moves + 2 * seqs;

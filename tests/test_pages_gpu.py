@@ -265,6 +265,23 @@ def test_the_largest_batch_page_and_number_of_pools(b):
         b.cache_reserve(i32([[5], [5]]), i32([9, 9]), i32([10, 10]), pools + some_pools(r, 8, [4]))
 
 
+@pytest.mark.parametrize("pages", [20000, 40000])
+def test_a_row_of_more_than_2_to_the_30_blocks(b, pages):
+    """Pages of one token, and a row so long that what is given lies past its 2^30-th entry: in the tables of a cluster and
+    in those of the workspace. The row lists the pages from 1 on, over and over."""
+    blocks, used = (1 << 30) + 70000, pages - 100
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda").remainder_(used).add_(1).view(1, blocks)
+    n = blocks - 50
+    want = table[0, -1000:].clone()
+    pool = torch.arange(pages, dtype=torch.int32, device="cuda").view(pages, 1)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, left = b.cache_reserve(table, i32([n]), i32([n + 10]), [pool], page_size=1, out=table, err_flag=err)
+    want[-50:-40] = i32([0] + list(range(used + 1, used + 10)))  # (the free ones: 0 and those behind the row's)
+    assert int(err) == 0 and int(left) == 90 and torch.equal(out[0, -1000:], want)
+    assert torch.equal(out[0, :1 << 20], torch.arange(1 << 20, dtype=torch.int32, device="cuda").remainder_(used).add_(1))
+    assert torch.equal(pool[:, 0], torch.arange(pages, dtype=torch.int32, device="cuda"))
+
+
 @pytest.mark.parametrize("n_pools", [16, 17])
 @pytest.mark.parametrize("batch,blocks,pages", [(20, 40, 900), (300, 40, 15000), (40, 40, 30000)])
 def test_many_pools_forks_and_too_few_pages(b, n_pools, batch, blocks, pages):
