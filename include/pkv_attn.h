@@ -634,7 +634,9 @@ int attn_cache_unpack_fp4(const void* k_pages, const void* v_pages, const int32_
  * q and out are bf16 and 16-byte aligned, lse, splits, workspace (attn_decode_workspace_size and
  * attn_decode_num_splits with PKV_FP4_E2M1) and err_flag as there. Group sizes 1 to 8.
  * Arithmetic: a code times its scale is exact in f16; q is scaled per head by a power of two and held in f16 as
- * in attn_decode_paged_fp8; a softmax weight enters the sum over V rounded to f16; sums and statistics are fp32.
+ * in attn_decode_paged_fp8; a softmax weight enters the sum over V rounded to f16, off by 2^-11 of itself or by 2^-32 of the
+ * largest (2^-25 where logits pass 2^20 in magnitude) before the division by their sum, which has them
+ * unrounded; sums and statistics are fp32. A row with logits past 2^23, where fp32 is in whole steps, may be NaN.
  * Slots behind a sequence's length do not matter, whatever bytes they hold. Both products run on the tensor
  * cores; there is no bounded wait in this call, so attn_debug_decode_stall does not act on it.
  */

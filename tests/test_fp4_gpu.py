@@ -312,6 +312,60 @@ def test_decode_scales_of_any_size(b, q_size, scale):
     close(out.float().cpu().numpy(), lse.cpu().numpy(), *want, lens, D, 6 * O.E4M3[0x4f] * np.abs(hs[1]).max())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_keeps_small_weights(b, D):
+    """Tails of keys whose weights are 2^-13, 2^-19 and 2^-26 of the largest one's, which each warp meets in its first
+    step and whose value is 0: what comes out is the tails'. A weight is held in f16 at 2^7 of what it is relative to the first
+    step's largest, so it is off by 2^-11 of itself or, below f16's normal range, by 2^-32 of that one."""
+    r = np.random.default_rng(27)
+    pages, lens = 48, [768, 761, 750]
+    codes_at, scale = 8 * D, 1.07 / math.log2(math.e)
+    k, v = (np.zeros((3 * pages, 1, 9 * D), dtype=np.uint8) for _ in range(2))
+    k[..., 0] = 0x07  # element 0 is 6 times its scale, the rest 0
+    s = {x: int(np.flatnonzero(O.E4M3 == x)[0]) for x in (12, 13, 14, 16)}
+    for i, tail in enumerate((14, 13, 12)):  # 12.8, 19.3 and 25.7 powers of two below the largest
+        k[i * pages:(i + 1) * pages, 0, codes_at:codes_at + 16] = s[tail]
+        v[i * pages:(i + 1) * pages, 0, :codes_at] = 0x22 + r.integers(0, 6, (pages, codes_at)) * 0x11 % 0x66
+        v[i * pages:(i + 1) * pages, 0, codes_at:] = r.integers(0x38, 0x50, (pages, D))
+        for w in range(4):  # a warp's first step: two pages
+            k[i * pages + 2 * w, 0, codes_at] = s[16]
+            v[i * pages + 2 * w, 0, codes_at::16] = 0
+    table = np.arange(3 * pages).reshape(3, pages)
+    q = torch.zeros(3, 2, D)
+    q[:, 0, 0], q[:, 1, 0] = 1.0, 0.984375
+    q = q.bfloat16()
+    out, lse = b.decode_paged_fp4(q.cuda(), gpu(k), gpu(v), i32(table), i32(lens), scale, num_splits=1)
+    want, want_lse, size, mass = O.decode(q.double().numpy(), k, v, None, None, table, lens, scale)
+    n = np.array(lens, dtype=np.float64)[:, None]
+    e = (D + 8) * 2.0 ** -24 * mass + 2.0 ** -20
+    top = np.exp(scale * 96 * q[:, :, 0].double().numpy() - want_lse)  # the largest weight
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * e + n * 2.0 ** -24)[..., None] * size + (n * 2.0 ** -32 * top)[..., None] * 48
+    got = out.double().cpu().numpy()
+    assert (want > 0).any((1, 2)).all() and (np.abs(got - want) <= tol).all()
+    assert (np.abs(lse.cpu().numpy() - want_lse) <= e + n * 2.0 ** -24 + 2.0 ** -21 * np.abs(want_lse)).all()
+
+
+@pytest.mark.parametrize("most", [2.0 ** 8, 2.0 ** 17, 2.0 ** 20, 2.0 ** 23])
+def test_decode_large_logits(b, most):
+    """Logits up to 2^23, whose steps there are as wide as a factor of two of a weight: results are means of V."""
+    r = np.random.default_rng(29)
+    D, lens = 64, [900, 200]
+    q, pools, table, bad, hs = make_decode(r, lens, 4, 2, D)
+    scale = most / O.decode(q.double().numpy(), *pools, *hs, table, lens, 1.0)[3].max()  # (of the sums of magnitudes)
+    scale = float(np.float32(scale))
+    want, want_lse, size, mass = O.decode(q.double().numpy(), *pools, *hs, table, lens, scale)
+    for splits in (1, 3):
+        out, lse = b.decode_paged_fp4(q.cuda(), gpu(pools[0]), gpu(pools[1]), i32(bad), i32(lens), scale, k_scale=gpu(hs[0]),
+                                      v_scale=gpu(hs[1]), num_splits=splits)
+        got = out.double().cpu().numpy()
+        # a logit's error makes other weights of the same sum: still a mean
+        assert np.isfinite(got).all() and (np.abs(got).max((1, 2)) <= 6 * O.E4M3[0x4f] * hs[1].max() * (1 + 2.0 ** -7)).all()
+        e = (D + 8) * 2.0 ** -24 * mass + 2.0 ** -20
+        assert (np.abs(lse.cpu().numpy() - want_lse) <= e + 900 * 2.0 ** -24 + 2.0 ** -21 * np.abs(want_lse)).all()
+        if most < 1000:
+            close(out.float().cpu().numpy(), lse.cpu().numpy(), want, want_lse, size, mass, lens, D, 6 * O.E4M3[0x4f] * hs[1].max())
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e30])
 def test_decode_queries_outside_f16(b, size):
     r = np.random.default_rng(13)
