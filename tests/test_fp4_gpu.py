@@ -366,6 +366,28 @@ def test_decode_large_logits(b, most):
             close(out.float().cpu().numpy(), lse.cpu().numpy(), want, want_lse, size, mass, lens, D, 6 * O.E4M3[0x4f] * hs[1].max())
 
 
+@pytest.mark.parametrize("scale,head,q_at", [(2.0 ** 100, 2.0 ** 29, -133), (2.0 ** -70, 2.0 ** -70, 122), (2.0 ** -120, 2.0 ** 20, 97),
+                                             (-2.0 ** 64, 2.0 ** 64, -128)])
+def test_decode_scale_times_head_scale_outside_fp32(b, scale, head, q_at):
+    """A scale and head scales whose product is no normal fp32 number, with queries of the opposite size: ordinary logits."""
+    r = np.random.default_rng(28)
+    D, lens = 128, [1, 40, 90]
+    q, pools, table, bad, hs = make_decode(r, lens, 4, 2, D)
+    for pool in pools:
+        live = pool[..., 8 * D:]
+        if q_at == 122:
+            live[live < 0x50] += 0x2e  # (products of 2^-140 need large keys)
+    hs[0] = (head * (1 + r.random(2))).astype(np.float32)
+    x = r.integers(-8, 9, (3, 4, D)).astype(np.float64) * 2.0 ** q_at
+    q = torch.tensor(x).to(torch.bfloat16)
+    assert (q.double().numpy() == x).all()
+    want = O.decode(x, *pools, *hs, table, lens, scale)
+    want = want[:3] + (np.abs(want[3]),)
+    out, lse = b.decode_paged_fp4(q.cuda(), gpu(pools[0]), gpu(pools[1]), i32(bad), i32(lens), scale, k_scale=gpu(hs[0]),
+                                  v_scale=gpu(hs[1]))
+    close(out.float().cpu().numpy(), lse.cpu().numpy(), *want, lens, D, 6 * 448 * hs[1].max())
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e30])
 def test_decode_queries_outside_f16(b, size):
     r = np.random.default_rng(13)
