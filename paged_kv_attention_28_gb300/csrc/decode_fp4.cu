@@ -164,8 +164,8 @@ __device__ __forceinline__ void convert_queries(const DecodeArgs& a, const uint3
   // Not 0, so that a masked product stays -inf as a logit; products are below 2^35, so what 2^-126 makes of them is 0.
   // The scale's power of two goes apart, in two factors: its product with the head's scale may be no fp32 number, or one of
   // few bits, where the query makes an ordinary logit of it.
-  const int up_by = a.scale_exponent - sh, half = up_by >> 1;
-  auto power = [](int e) { return __uint_as_float((uint32_t)(127 + min(max(e, -126), 127)) << 23); };
+  const int up_by = a.scale_exponent - sh, half = up_by >> 1;  // (-250 .. 243)
+  auto power = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
   const float unscale = a.scale_fraction * fabsf(k_scale) * power(half) * power(up_by - half);
   if (part == 0) to.scale[h] = unscale < 1.17549435e-38f ? 1.17549435e-38f : unscale;
 }
@@ -593,6 +593,7 @@ int launch_t(DecodeArgs a, cudaStream_t stream) {
   // (below 1, so that its product with a head's scale is finite)
   a.scale_fraction = 0.5f * kLog2e * std::frexp(std::fabs(a.scale), &a.scale_exponent);
   ++a.scale_exponent;
+  if (a.scale_exponent < -124) a.scale_fraction = std::ldexp(a.scale_fraction, a.scale_exponent + 124), a.scale_exponent = -124;
   const int ctas = a.n_kv_heads * a.num_splits;
   const bool ordered = is_ordered(a.batch, a.n_kv_heads, a.num_splits, a.pages_per_split, a.sms, Cfg<D>::kCtas);
   auto* kernel = ordered ? decode_fp4_kernel<D, true> : decode_fp4_kernel<D, false>;
