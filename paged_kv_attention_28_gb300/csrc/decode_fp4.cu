@@ -366,26 +366,22 @@ struct Attention {
   }
 };
 
-// Whether the stream's next kernel may be placed before this one's end: the merge, or whatever follows a launch of more CTAs than
-// fit. One-wave launches that begin early get their CTAs where the kernel before leaves room, unevenly for good (40 x
-// 100-1000 tokens of 8 heads, calls one after another, 14.4 us and 11.7), so other launches leave the next one alone.
-__device__ __forceinline__ bool lets_next(const DecodeArgs& a) { return a.num_splits > 1 || gridDim.x * gridDim.y > 4 * a.sms; }
-
 // What a CTA works on where the lengths order the CTAs: the splits of 128 (sequence, split) pairs, most pages first, each with
 // all its KV heads; then of the next 128 pairs, and what is left over of the batch comes first of all. Those of the SMs' first
 // CTAs (sms at a time) are taken from either end in turn, so that no SM gets the longest of all.
 struct Place {
   int item, head;  // item: sequence * num_splits + split
 };
+template <int D>
 __device__ __forceinline__ Place place_of(const DecodeArgs& a) {
   __shared__ __align__(16) uint32_t keys[kGroup];
   __shared__ int found;
   const int t = threadIdx.x, p0 = blockIdx.x, layer = p0 / a.sms;
-  const int p = layer < 4 && (layer & 1) ? min((int)gridDim.x, (layer + 1) * a.sms) - 1 - (p0 - layer * a.sms) : p0;
+  const int p = layer < Cfg<D>::kCtas && (layer & 1) ? min((int)gridDim.x, (layer + 1) * a.sms) - 1 - (p0 - layer * a.sms) : p0;
   const int place = p / a.n_kv_heads, n = a.batch * a.num_splits, odd = n % kGroup;
   const int begin = place < odd ? 0 : odd + (place - odd) / kGroup * kGroup, count = place < odd ? odd : kGroup;
   wait_for_stream();
-  if (lets_next(a)) let_next_start();  // (after the wait: the merge reads the lengths at once)
+  if (a.lets_next) let_next_start();  // (after the wait: the merge reads the lengths at once)
   uint32_t key = 0;
   if (t < count) {
     const int split = (begin + t) % a.num_splits, len = __ldg(a.kv_lens + (begin + t) / a.num_splits);
@@ -417,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<D>::kWarps * 32, Cfg<D>::kCtas) decode_fp4
   const int per = a.pages_per_split, G = a.n_qo_heads / a.n_kv_heads;
   int b, head, split;
   if constexpr (ORDERED) {
-    const Place at = place_of(a);
+    const Place at = place_of<D>(a);
     b = at.item / a.num_splits, split = at.item % a.num_splits, head = at.head;
   } else {
     // Every other sequence's CTAs in reverse: those of splits that a sequence has not, which end at once, are then not
@@ -426,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<D>::kWarps * 32, Cfg<D>::kCtas) decode_fp4
     const int x = b & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
     head = x % a.n_kv_heads, split = x / a.n_kv_heads;
     wait_for_stream();
-    if (lets_next(a)) let_next_start();  // (after the wait: the merge reads the lengths at once)
+    if (a.lets_next) let_next_start();  // (after the wait: the merge reads the lengths at once)
   }
 
   __shared__ __align__(16) Queries<D> queries;
@@ -598,6 +594,10 @@ int launch_t(DecodeArgs a, cudaStream_t stream) {
   const bool ordered = is_ordered(a.batch, a.n_kv_heads, a.num_splits, a.pages_per_split, a.sms, Cfg<D>::kCtas);
   auto* kernel = ordered ? decode_fp4_kernel<D, true> : decode_fp4_kernel<D, false>;
   if (!configured[ordered].ensure(reinterpret_cast<const void*>(kernel), Cfg<D>::kSmem)) return PKV_ERR_LAUNCH;
+  // Whether the stream's next kernel may be placed before this one's end: the merge, or whatever follows a launch of more CTAs than
+  // fit. One-wave launches that begin early get their CTAs where the kernel before leaves room, unevenly for good (40 x
+  // 100-1000 tokens of 8 heads, calls one after another, 14.4 us and 11.7), so other launches leave the next one alone.
+  a.lets_next = a.num_splits > 1 || (int64_t)ctas * a.batch > (int64_t)Cfg<D>::kCtas * a.sms;
   const dim3 grid = ordered ? dim3((unsigned)ctas * a.batch) : dim3((unsigned)ctas, (unsigned)a.batch);
   const int rc = check_launch(launch_overlapped(kernel, grid, Cfg<D>::kWarps * 32, Cfg<D>::kSmem, stream, 1, a));
   if (rc != PKV_OK || a.num_splits == 1) return rc;

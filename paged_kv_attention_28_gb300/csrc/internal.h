@@ -53,9 +53,10 @@ struct DecodeArgs {
   // Accumulated weights: where the logits (base-2 units) of every key go, fp32
   // [batch][n_qo_heads][max_blocks * page_size]; null: not wanted.
   float* logits = nullptr;
-  // 4-bit pages: the device's SMs; |scale| log2(e) as fraction * 2^exponent
+  // 4-bit pages: the device's SMs; |scale| log2(e) as fraction * 2^exponent; whether the next kernel may be placed early
   int sms, scale_exponent;
   float scale_fraction;
+  bool lets_next;
 };
 
 
