@@ -105,7 +105,7 @@ SplitPlan plan_decode_splits(int batch, int max_blocks, int n_kv_heads, int requ
 static SplitPlan plan_decode(int batch, int max_blocks, int n_qo_heads, int n_kv_heads, int head_dim, int page_size,
                       int num_splits, int dtype) {
   const int G = n_qo_heads / n_kv_heads;
-  if (dtype == PKV_FP4_E2M1) return plan_decode_fp4(batch, max_blocks, n_kv_heads, head_dim, num_splits);
+  if (dtype == PKV_FP4_E2M1) return plan_decode_fp4(batch, max_blocks, n_kv_heads, num_splits);
   if (dtype == PKV_FP8_E4M3) {
     DecodeArgs d{};
     d.n_qo_heads = n_qo_heads;
@@ -633,7 +633,7 @@ int attn_decode_paged_fp4(const void* q, const void* k_pages, const void* v_page
   if ((head_dim != 64 && head_dim != 128) || page_size != 16 || n_qo_heads / n_kv_heads > 8 || batch > 65535 || n_kv_heads > 65535 ||
       (long)max_blocks_per_seq * page_size > kMaxTokens)
     return PKV_ERR_UNSUPPORTED;
-  const SplitPlan plan = plan_decode_fp4(batch, max_blocks_per_seq, n_kv_heads, head_dim, num_splits);
+  const SplitPlan plan = plan_decode_fp4(batch, max_blocks_per_seq, n_kv_heads, num_splits);
   if ((long)n_kv_heads * plan.num_splits > 0x7fffffffL || (long)batch * n_qo_heads > 0x7fffffffL) return PKV_ERR_UNSUPPORTED;
   const size_t need = decode_ws_bytes(batch, n_qo_heads, n_kv_heads, head_dim, plan.num_splits);
   if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))

@@ -608,8 +608,8 @@ int launch_t(DecodeArgs a, cudaStream_t stream) {
 
 constexpr double kFixed = 12;
 
-// Estimated time of so many splits, in pages that an SM goes through (65 ns each at head_dim 128), where `filled` of the CTAs
-// have pages: each takes its pages and a fixed cost of kFixed (its first loads, the warps' states), fewer than four on an SM
+// Estimated time of so many splits, in pages that an SM goes through (65 ns each at head_dim 128, and the same pages are
+// counted at head_dim 64, where they take less: see below), where `filled` of the CTAs have pages: each takes its pages and a fixed cost of kFixed (its first loads, the warps' states), fewer than four on an SM
 // are slower, and a second launch is kMerge and something for each split. Whole CTAs, or on average.
 static double time_of_splits(double units, int max_blocks, int s, double filled, bool whole, int sms, int ctas) {
   constexpr double kMerge = 40;
@@ -627,16 +627,18 @@ static double time_of_splits(double units, int max_blocks, int s, double filled,
 // of full rows and that of rows 3/5 full on average, where the last CTAs run alone for some of their pages, together.
 // Measured (us, the chosen one first): 4 x 32768 tokens of 8 heads 30.6 with 19 splits, 33.4 with 32, 33.9 with 38; the same
 // with 6000-32768 tokens 24.7 with 19, 25.5 with 32, 28.3 with 38; 16 x 512-4096 of 32 heads 37.8 with 2, 40.2 with 4, 49.9
-// with 1; 64 x 100-1000 of 8 15.5 with 1, 19.3 with 2. CTAs that find the lengths and divide the pages evenly among them
+// with 1; 64 x 100-1000 of 8 15.5 with 1, 19.3 with 2. Head_dim 64, 8 shapes of full rows and of ragged ones: within 9 % of the best
+// of up to 20 counts but for 8 x 1000-10000 tokens of 8 heads, 15.0 with 9 splits and 12.5 with 16. CTAs that find the lengths and divide the pages evenly among them
 // do so whatever they are, but take 2 us more (33.7, 25.6 and 45.8 us for the first three).
-SplitPlan plan_decode_fp4(int batch, int max_blocks, int n_kv_heads, int head_dim, int requested) {
+SplitPlan plan_decode_fp4(int batch, int max_blocks, int n_kv_heads, int requested) {
   int S;
   if (requested > 0) {
     S = requested < max_blocks ? requested : max_blocks;
   } else {
     int sms = device_sm_count();
     if (sms <= 0) sms = 148;
-    const int ctas = head_dim == 128 ? Cfg<128>::kCtas : Cfg<64>::kCtas, most = max_blocks < 128 ? max_blocks : 128;
+    static_assert(Cfg<64>::kCtas == Cfg<128>::kCtas, "one estimate for both");
+    const int ctas = Cfg<128>::kCtas, most = max_blocks < 128 ? max_blocks : 128;
     const double units = (double)batch * n_kv_heads;
     double best = -1;
     S = 1;

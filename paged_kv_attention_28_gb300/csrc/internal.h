@@ -280,7 +280,7 @@ struct Fp4CopyArgs {
 int launch_fp4_copy(const Fp4CopyArgs& a, cudaStream_t stream);
 
 // Decode over 4-bit pages (decode_fp4.cu). a.k_scale, a.v_scale: [n_kv_heads] or null; a.dtype: PKV_BF16.
-SplitPlan plan_decode_fp4(int batch, int max_blocks, int n_kv_heads, int head_dim, int requested);
+SplitPlan plan_decode_fp4(int batch, int max_blocks, int n_kv_heads, int requested);
 int launch_decode_fp4(const DecodeArgs& a, cudaStream_t stream);
 // The merge of a decode's split partials (decode.cu).
 int launch_merge_splits(const DecodeArgs& a, cudaStream_t stream);
