@@ -183,7 +183,7 @@ __device__ __forceinline__ Block block_of(const Fp4CopyArgs& a, int per_block) {
   return k;
 }
 
-// Consecutive tokens of a lane: two, whose next rows are on their way meanwhile, are 37 us where four are 40 for 41k tokens of
+// Consecutive tokens of a lane. Packing, two, whose next rows are on their way meanwhile, are 37 us where four are 40 for 41k tokens of
 // 8 heads.
 constexpr int rows_of_lane(bool pack) { return pack ? 2 : 4; }
 
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, PACK ? 8 : 10) fp4_copy_kernel(const
   constexpr int R = rows_of_lane(PACK), kLanes = Tile::kGroups * Tile::kTokens / R;  // lanes of a tile
   constexpr int kTiles = kThreads / kLanes;  // tiles of a CTA at a time: K and V of kTiles / 2 heads
   static_assert(kTiles % 2 == 0, "a lane stays with K or V from turn to turn");
-  static_assert(PACK ? R == 2 || R == 4 : R == 4, "its scales are one aligned access");
+  static_assert(R == (PACK ? 2 : 4), "its scales are one aligned access, a half-word or a word");
   wait_for_stream();  // (the next kernel is not let in early: a decode's CTAs would be placed unevenly, 17.2 us for both, not 14.0)
   const Block k = block_of(a, per_block);
   if (!k.any) return;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, PACK ? 8 : 10) fp4_copy_kernel(const
         load(now, head);
       }
       const float inv_head = __frcp_rn(hs);
-      uint32_t s4 = 0;
+      uint32_t both = 0;
       bool all = true;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -266,17 +266,14 @@ __global__ void __launch_bounds__(kThreads, PACK ? 8 : 10) fp4_copy_kernel(const
         now[i].get(x);
         uint32_t s;
         *reinterpret_cast<uint2*>(codes + i * Tile::kRow) = quantise(x, inv_head, s);
-        s4 |= s << (8 * i);
+        both |= s << (8 * i);
       }
       if (all) {
-        if constexpr (R == 4)
-          *reinterpret_cast<uint32_t*>(lane_scales) = s4;
-        else
-          *reinterpret_cast<uint16_t*>(lane_scales) = (uint16_t)s4;
+        *reinterpret_cast<uint16_t*>(lane_scales) = (uint16_t)both;
       } else {
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          if (at[i] >= 0) lane_scales[i] = (char)(s4 >> (8 * i));
+          if (at[i] >= 0) lane_scales[i] = (char)(both >> (8 * i));
       }
     } else {
       uint32_t s4 = 0x7f7f7f7fu;  // a bad page: NaN
