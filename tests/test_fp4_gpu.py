@@ -237,6 +237,38 @@ def test_decode_long_and_many_pages_of_a_warp(b):
         close(out.float().cpu().numpy(), lse.cpu().numpy(), *want, lens, 64, 6 * O.E4M3[0x4f] * hs[1].max())
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (6, 2)])
+def test_decode_long_at_head_dim_128(b, Hq, Hkv):
+    """More than 32 pages of one warp where its ring has two steps; the same entries as one CTA's and as many splits'."""
+    r = np.random.default_rng(30)
+    D, lens = 128, [5000, 2065, 4111]
+    q, pools, table, bad, hs = make_decode(r, lens, Hq, Hkv, D)
+    want = O.decode(q.float().numpy(), *pools, *hs, table, lens, 0.04)
+    for splits in (1, 2, 5, 0):
+        out, lse = b.decode_paged_fp4(q.cuda(), gpu(pools[0]), gpu(pools[1]), i32(bad), i32(lens), 0.04, k_scale=gpu(hs[0]),
+                                      v_scale=gpu(hs[1]), num_splits=splits)
+        close(out.float().cpu().numpy(), lse.cpu().numpy(), *want, lens, D, 6 * O.E4M3[0x4f] * hs[1].max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("block", [127, 128, 200, 257, 312])
+def test_decode_bad_page_far_into_a_row(b, D, block):
+    """A bad entry that a warp meets in its first load of table entries (block 127) and in later ones."""
+    r = np.random.default_rng(31)
+    lens = [300, 5000, 4900]
+    q, pools, table, bad, hs = make_decode(r, lens, 2, 1, D, poison=False)
+    args = q.cuda(), gpu(pools[0]), gpu(pools[1])
+    for splits in (1, 2):
+        clean, clean_lse = b.decode_paged_fp4(*args, i32(bad), i32(lens), 0.1, num_splits=splits)
+        for entry in (-1, len(pools[0]), 1 << 30):
+            broken = bad.copy()
+            broken[1, block] = entry
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out, lse = b.decode_paged_fp4(*args, i32(broken), i32(lens), 0.1, num_splits=splits, err_flag=err)
+            assert int(err) == b.PKV_DEVERR_BAD_PAGE and out[1].isnan().all() and lse[1].isnan().all()
+            assert torch.equal(out[[0, 2]], clean[[0, 2]]) and torch.equal(lse[[0, 2]], clean_lse[[0, 2]])
+
+
 @pytest.mark.parametrize("B,Hkv,D,most", [(3, 2, 64, 4000), (40, 8, 64, 700), (129, 2, 128, 60), (300, 3, 64, 90), (1000, 1, 64, 20)])
 def test_decode_many_sequences(b, B, Hkv, D, most):
     """Ragged batches with sequences without tokens at any place; the library's splits against one."""
@@ -367,7 +399,7 @@ def test_decode_large_logits(b, most):
 
 
 @pytest.mark.parametrize("scale,head,q_at", [(2.0 ** 100, 2.0 ** 29, -133), (2.0 ** -70, 2.0 ** -70, 122), (2.0 ** -120, 2.0 ** 20, 97),
-                                             (-2.0 ** 64, 2.0 ** 64, -128)])
+                                             (-2.0 ** 64, 2.0 ** 64, -128), (2.0 ** -140, 2.0 ** 35, 100)])
 def test_decode_scale_times_head_scale_outside_fp32(b, scale, head, q_at):
     """A scale and head scales whose product is no normal fp32 number, with queries of the opposite size: ordinary logits."""
     r = np.random.default_rng(28)
