@@ -12,9 +12,10 @@
 // pages a CTA takes several heads of a page in turn, so that the tables are looked at once for all of them.
 //
 // Both are bound by memory, packing also by its loads in flight (54 % of the issue slots; 32 warps an SM, for which it spills 16
-// bytes, are 2 to 5 % faster than the 28 of its 71 registers, 40 spill more: 44 us for 37.8). 41k tokens of 8 heads of 128
-// packed from bf16: 37.1 us, 215 MB, 5.8 TB/s; 64k tokens back to bf16: 55.2 us, 344 MB, 6.2 TB/s. A step's token of each
-// of 64 sequences: 2.9 us, a launch.
+// bytes from bf16 and 28 from fp32, are 2 to 5 % faster from bf16 than the 28 of its 71 registers, 40 spill more: 44 us for 37.8). 41k
+// tokens of 8 heads of 128 packed from bf16: 37.1 us, 215 MB, 5.8 TB/s; from fp32, whose rows are twice the bytes in flight and not
+// asked for ahead: 60.9 us, 383 MB, 6.3 TB/s. 64k tokens back to bf16: 55.2 us, 344 MB, 6.2 TB/s; to fp32 96.0, 612 MB, 6.4. Head_dim 64 (half
+// the bytes of 41k tokens): 21.7 and 33.8 us. A step's token of each of 64 sequences: 2.9 us, a launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
