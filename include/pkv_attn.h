@@ -589,15 +589,15 @@ int attn_linear(const void* x, const void* w, const void* bias, const void* resi
  *                      codes [16][head_dim / 2] (element 2 i of a token in the low half of byte i,
  *                      2 i + 1 in the high half), then scales [head_dim / 16][16] (by group, then by
  *                      token); 16-byte aligned
- *   k_scale, v_scale : fp32 [n_kv_heads], finite and not 0, or NULL (1 for every head). A head's largest
- *                      magnitude over 2688 (6 * 448) uses the whole range of the scales
+ *   k_scale, v_scale : fp32 [n_kv_heads], finite and at least 2^-126 in magnitude, or NULL (1 for every head). A
+ *                      head's largest magnitude over 2688 (6 * 448) uses the whole range of the scales
  *
  * attn_cache_pack_fp4 writes tokens of ordinary pages into 4-bit pages: new tokens that
  * attn_qk_norm_rope_append has put into the pages of a step, or a prompt after its prefill. Token i of
  * sequence b, i < counts[b], goes from position src_first[b] + i of src_table's pages to position
  * first[b] + i of block_table's. For each 16 elements x, with one rounding (to nearest even) a step:
  *   y = x * (1 / head scale);  s = e4m3(max |y| * (1 / 6)), at most 448;  code = e2m1(y * (1 / s)), at most 6
- * s = 0 has codes 0. An element that is not finite makes its group's scale NaN: all 16 read as NaN.
+ * s = 0 has codes 0. An element whose y is not finite makes its group's scale NaN: all 16 read as NaN.
  *
  * attn_cache_unpack_fp4 reads tokens back into ordinary pages, where attn_prefill_paged_chunk and the
  * other calls take them: x = (e2m1(code) * e4m3(s)) * head scale, rounded once more to the type of the pages.

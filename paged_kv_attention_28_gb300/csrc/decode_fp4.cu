@@ -26,9 +26,10 @@
 // halve what is not work on codes: waits, addresses, the look at the reference value.
 //
 // A page is 260 instructions and 102 clocks of an SM in the middle of a long split, which is 6.4 TB/s. 151 MB (4 x 32768
-// tokens of 8 heads) are 30.6 us: 1.5 until the first copies are issued, 23.5 of steps, 0.8 for the warps' states, 1.4
+// tokens of 8 heads) are 30.6 to 31 us: 1.5 until the first copies are issued, 23.5 of steps, 0.8 for the warps' states, 1.4
 // in which only some of an SM's CTAs are left, and the merge of the splits. 170 MB of unequal rows (16 x 512-4096 of 32
-// heads) are 37.8, at 55 % of the issue slots while an SM works. A cluster that puts up to 8 splits' states together in
+// heads) are 37.6, at 56 % of the issue slots while an SM works, 86 % of the time (128 registers a thread at D = 128; ordered by
+// length, 4 bytes of them are spilled). A cluster that puts up to 8 splits' states together in
 // shared memory, with no second launch, takes 0.2 to 0.7 us less where there are few CTAs, but its CTAs start
 // together: the second of these batches was 51 us with it and 41 without. So splits always meet in the merge.
 #include <cuda_bf16.h>
